@@ -355,6 +355,109 @@ int moe_mxfp4_layer_noalloc(const uint16_t* x_bf16, const float* logits, int T, 
                             void* stream);
 
 /*
+ * mxfp4_gemm — product of two MXFP4 matrices.
+ *   a_codes [M, K/2], a_scales [M, K/32], b_codes [N, K/2], b_scales [N, K/32]
+ *           uint8 as mxfp4_pack writes them, read; codes 16-byte aligned,
+ *           scales unaligned
+ *   c       [M, N] f32 or bf16 (c_dtype), written:
+ *           c[m, n] = sum_k a[m, k] * b[n, k]; aligned to its elements
+ * Products are exact and accumulated in fp32; bf16 is rounded once at the end
+ * (RNE).  Every scale byte is taken as mxfp4_unpack takes it: 0 is 2^-127 and
+ * 255 makes the rows (columns) it belongs to NaN; where the products'
+ * magnitudes sum past fp32's range the result may be Inf or NaN.
+ * Deterministic.  K a
+ * multiple of 32 from 32 to 2^20; any M and N, 0 being a no-op.
+ * The pages store weights in MXFP4 (model card, §2 "FP4 Quantization") and
+ * keep activations in higher precision; MXFP4 activations are an addition.
+ */
+int mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+               const uint8_t* b_scales, int M, int N, int K, void* c, int c_dtype, void* stream);
+
+/*
+ * moe_mxfp4_a4_gate_up_swiglu — moe_mxfp4_gate_up_swiglu on MXFP4
+ * activations.
+ *   x_codes [T, H/2], x_scales [T, H/32] uint8 (mxfp4_pack of the tokens)
+ *   sorted_pairs, offsets, w13_codes, w13_scales: as there
+ *   h_bf16  [T*k, I] bf16, written as there; or NULL, and then
+ *   h_codes [T*k, I/2], h_scales [T*k, I/32] uint8, written: mxfp4_pack of
+ *           that h (of its bf16 values), bit for bit.  Exactly one of h_bf16
+ *           and the pair is given; anything else is MXM_ERR_NULL.
+ * For row r of expert e with token t = sorted_pairs[r] / k: g = W_gate,e x_t
+ * and u = W_up,e x_t with exact products accumulated in fp32, h_r =
+ * bf16_rne(silu(g) * u).  Scale bytes as mxfp4_gemm takes them (0 and 255
+ * included, unlike the bf16-activation call).  Rows at and past offsets[E]
+ * are left as they were.  Codes and h 16-byte aligned, scales unaligned.
+ */
+int moe_mxfp4_a4_gate_up_swiglu(const uint8_t* x_codes, const uint8_t* x_scales,
+                                const int32_t* sorted_pairs, const int32_t* offsets, int T, int H,
+                                int I, int E, int k, const uint8_t* w13_codes,
+                                const uint8_t* w13_scales, uint16_t* h_bf16, uint8_t* h_codes,
+                                uint8_t* h_scales, void* stream);
+
+/*
+ * moe_mxfp4_a4_down — moe_mxfp4_down on MXFP4 activations.
+ *   h_codes [T*k, I/2], h_scales [T*k, I/32] uint8, read
+ *   offsets, w2_codes, w2_scales, y: as there
+ * y_r = W_down,e h_r, exact products accumulated in fp32.  Scale bytes,
+ * alignment and rows past offsets[E] as moe_mxfp4_a4_gate_up_swiglu.
+ */
+int moe_mxfp4_a4_down(const uint8_t* h_codes, const uint8_t* h_scales, const int32_t* offsets,
+                      int T, int H, int I, int E, int k, const uint8_t* w2_codes,
+                      const uint8_t* w2_scales, float* y, void* stream);
+
+/*
+ * moe_mxfp4_a4_layer — moe_mxfp4_layer with MXFP4 activations on both
+ * contractions: enqueues moe_route_permute, mxfp4_pack of x,
+ * moe_mxfp4_a4_gate_up_swiglu (writing h in MXFP4), moe_mxfp4_a4_down and
+ * moe_combine, with the caller's buffers (those of moe_mxfp4_layer, with
+ * x_codes [T, H/2], x_scales [T, H/32], h_codes [T*k, I/2], h_scales
+ * [T*k, I/32] in place of h_bf16).  Results are those of the separate calls,
+ * bit for bit.  Errors as moe_mxfp4_layer.
+ */
+int moe_mxfp4_a4_layer(const uint16_t* x_bf16, const float* logits, int T, int H, int I, int E,
+                       int k, const uint8_t* w13_codes, const uint8_t* w13_scales,
+                       const uint8_t* w2_codes, const uint8_t* w2_scales, int32_t* topk_ids,
+                       float* topk_w, int32_t* counts, int32_t* offsets, int32_t* sorted_pairs,
+                       int32_t* pair_to_row, uint8_t* x_codes, uint8_t* x_scales,
+                       uint8_t* h_codes, uint8_t* h_scales, float* y, float* out,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace dflash_verify_probs needs (0 for invalid sizes). */
+size_t dflash_verify_probs_workspace_bytes(int B, int L, int V);
+
+/*
+ * dflash_verify_probs — dflash_verify_accept from probabilities, for callers
+ * that shape the target's distribution first (temperature, truncation), with
+ * blocks of unequal length.
+ *   target_probs [B, L+1, V], draft_probs [B, L, V] f32 or bf16 (dtype, the
+ *                same for both), read
+ *   draft_tokens [B, L] int32, read
+ *   draft_len    [B] int32, read: block b has draft_len[b] tokens (clamped to
+ *                0..L); NULL: L each
+ *   uniforms     [B, L+1] f32 in [0, 1), read: one per position, the last of
+ *                a row (index L) for its draw
+ *   accept_len   [B] int32, written: n, the leading positions accepted
+ *   next_token   [B] int32, written: the token after the n accepted ones
+ *   workspace    dflash_verify_probs_workspace_bytes(B, L, V) bytes, 8-byte
+ *                aligned; its contents need no initialisation.  Calls that
+ *                share one must not overlap.
+ * Rule of dflash_verify_accept with p_i = target_probs[b, i] and q_i =
+ * draft_probs[b, i] as given: they need not sum to 1, and an entry that is
+ * not a positive finite number counts as 0.  After a whole block
+ * (n = draft_len) the token is drawn from p_n.  Where p_n has no positive
+ * entry there is no token: next_token is -1.  A drafted token outside [0, V)
+ * is rejected.  Acceptance is decided exactly; sums are in fp64 in a fixed
+ * order, so a draw may differ from exact arithmetic only within 2^-35 of a
+ * boundary, relative to the sum.  1 <= L <= 32, 1 <= V <= 2^30, B <= 2^24.
+ * Elements need only their own alignment.
+ */
+int dflash_verify_probs(const void* target_probs, const void* draft_probs, int dtype,
+                        const int32_t* draft_tokens, const int32_t* draft_len,
+                        const float* uniforms, int B, int L, int V, int32_t* accept_len,
+                        int32_t* next_token, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/*
  * mxm_stream_xor — measurement aid, not a step of the layer: a plain
  * streaming read of `bytes` bytes at `src` (16-byte aligned, bytes % 16 == 0)
  * that XORs every 32-bit word into *result (4-byte aligned; the caller sets

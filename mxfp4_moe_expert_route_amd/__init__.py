@@ -11,6 +11,8 @@ from .ops import (  # noqa: F401
     decode_layer_workspace,
     moe_permute, moe_permute_workspace_bytes, moe_route_permute, moe_route_topk, moe_router_topk, mxfp4_pack,
     mxfp4_unpack, mxm_stream_xor,
+    A4LayerBuffers, dflash_verify_probs, dflash_verify_probs_workspace_bytes, moe_mxfp4_a4_down,
+    moe_mxfp4_a4_gate_up_swiglu, moe_mxfp4_a4_gate_up_swiglu_pack, moe_mxfp4_a4_layer, mxfp4_gemm,
 )
 
 MXM_F32, MXM_BF16 = 0, 1

@@ -37,6 +37,17 @@ SIGNATURES = {
                                         _p]),
     "moe_mxfp4_layer_noalloc": (_c_int, [_p, _p, _c_int, _c_int, _c_int, _c_int, _c_int, _p, _p,
                                          _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p]),
+    "mxfp4_gemm": (_c_int, [_p, _p, _p, _p, _c_int, _c_int, _c_int, _p, _c_int, _p]),
+    "moe_mxfp4_a4_gate_up_swiglu": (_c_int, [_p, _p, _p, _p, _c_int, _c_int, _c_int, _c_int,
+                                             _c_int, _p, _p, _p, _p, _p, _p]),
+    "moe_mxfp4_a4_down": (_c_int, [_p, _p, _p, _c_int, _c_int, _c_int, _c_int, _c_int, _p, _p, _p,
+                                   _p]),
+    "moe_mxfp4_a4_layer": (_c_int, [_p, _p, _c_int, _c_int, _c_int, _c_int, _c_int, _p, _p, _p, _p,
+                                    _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _c_size,
+                                    _p]),
+    "dflash_verify_probs_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int]),
+    "dflash_verify_probs": (_c_int, [_p, _p, _c_int, _p, _p, _p, _c_int, _c_int, _c_int, _p, _p,
+                                     _p, _c_size, _p]),
     "moe_mxfp4_layer": (_c_int, [_p, _p, _c_int, _c_int, _c_int, _c_int, _c_int, _p, _p, _p, _p,
                                  _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _c_size, _p]),
 }

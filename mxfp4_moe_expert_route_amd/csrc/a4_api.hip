@@ -1,0 +1,167 @@
+// C ABI of the products of two MXFP4 factors, of the layer on MXFP4
+// activations and of verification from probabilities: host-side argument
+// checks, then launches.  As in api.hip, every check runs before anything is
+// enqueued and none of them touches the HIP runtime.
+#include "../../include/mxfp4moe.h"
+#include "a4.hpp"
+
+namespace {
+
+using mxm::a4::Problem;
+
+constexpr int kMaxE = 1024;
+constexpr int kMaxK = 32;
+constexpr int kMaxH = 16384;
+constexpr int kMaxI = 8192;
+constexpr int kMaxGemmK = 1 << 20;
+constexpr int kMaxVerifyL = 32;          // one lane of a wave per block position
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int launched(hipError_t e) { return e == hipSuccess ? MXM_OK : MXM_ERR_LAUNCH; }
+
+hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
+
+int check_ffn_shape(int T, int H, int I, int E, int k) {
+  if (T < 0 || E < 1 || E > kMaxE || k < 1 || k > kMaxK || k > E) return MXM_ERR_SHAPE;
+  if (int64_t(T) * k > INT32_MAX) return MXM_ERR_SHAPE;
+  if (H < 32 || I < 32 || H % 32 || I % 32 || H > kMaxH || I > kMaxI) return MXM_ERR_SHAPE;
+  return MXM_OK;
+}
+
+// Where the contraction runs (decided from sizes alone).
+hipError_t contract(mxm::a4::Kind kind, mxm::a4::Out out, const Problem& p, hipStream_t s) {
+  return mxm::a4::launch_direct(kind, out, p, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+int mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+               const uint8_t* b_scales, int M, int N, int K, void* c, int c_dtype, void* stream) {
+  if (c_dtype != MXM_F32 && c_dtype != MXM_BF16) return MXM_ERR_DTYPE;
+  if (M < 0 || N < 0 || K < 32 || K % 32 || K > kMaxGemmK) return MXM_ERR_SHAPE;
+  if (M == 0 || N == 0) return MXM_OK;
+  if (!a_codes || !a_scales || !b_codes || !b_scales || !c) return MXM_ERR_NULL;
+  if (!aligned(a_codes, 16) || !aligned(b_codes, 16) || !aligned(c, c_dtype == MXM_F32 ? 4 : 2))
+    return MXM_ERR_ALIGN;
+  Problem p{};
+  p.xc = a_codes; p.xs = a_scales; p.wc = b_codes; p.ws = b_scales;
+  p.out = c;
+  p.M = M; p.R = M; p.N = N; p.K = K; p.E = 1; p.k = 1;
+  p.lo = 1; p.hi = INT32_MAX;
+  return launched(contract(mxm::a4::kGemm, c_dtype == MXM_F32 ? mxm::a4::kF32 : mxm::a4::kBf16, p,
+                           as_stream(stream)));
+}
+
+int moe_mxfp4_a4_gate_up_swiglu(const uint8_t* x_codes, const uint8_t* x_scales,
+                                const int32_t* sorted_pairs, const int32_t* offsets, int T, int H,
+                                int I, int E, int k, const uint8_t* w13_codes,
+                                const uint8_t* w13_scales, uint16_t* h_bf16, uint8_t* h_codes,
+                                uint8_t* h_scales, void* stream) {
+  const int st = check_ffn_shape(T, H, I, E, k);
+  if (st != MXM_OK) return st;
+  if (T == 0) return MXM_OK;
+  const bool mx = h_codes || h_scales;
+  if (!x_codes || !x_scales || !sorted_pairs || !offsets || !w13_codes || !w13_scales ||
+      (mx ? !h_codes || !h_scales || h_bf16 : !h_bf16))
+    return MXM_ERR_NULL;
+  if (!aligned(x_codes, 16) || !aligned(w13_codes, 16) || !aligned(h_bf16, 16) ||
+      !aligned(h_codes, 16) || !aligned(sorted_pairs, 4) || !aligned(offsets, 4))
+    return MXM_ERR_ALIGN;
+  Problem p{};
+  p.xc = x_codes; p.xs = x_scales; p.wc = w13_codes; p.ws = w13_scales;
+  p.pairs = sorted_pairs; p.offsets = offsets;
+  p.out = h_bf16; p.oc = h_codes; p.os = h_scales;
+  p.M = T; p.R = T * k; p.N = I; p.K = H; p.E = E; p.k = k;
+  p.lo = 1; p.hi = INT32_MAX;
+  return launched(contract(mxm::a4::kGateUp, mx ? mxm::a4::kMx : mxm::a4::kBf16, p,
+                           as_stream(stream)));
+}
+
+int moe_mxfp4_a4_down(const uint8_t* h_codes, const uint8_t* h_scales, const int32_t* offsets,
+                      int T, int H, int I, int E, int k, const uint8_t* w2_codes,
+                      const uint8_t* w2_scales, float* y, void* stream) {
+  const int st = check_ffn_shape(T, H, I, E, k);
+  if (st != MXM_OK) return st;
+  if (T == 0) return MXM_OK;
+  if (!h_codes || !h_scales || !offsets || !w2_codes || !w2_scales || !y) return MXM_ERR_NULL;
+  if (!aligned(h_codes, 16) || !aligned(w2_codes, 16) || !aligned(y, 16) || !aligned(offsets, 4))
+    return MXM_ERR_ALIGN;
+  Problem p{};
+  p.xc = h_codes; p.xs = h_scales; p.wc = w2_codes; p.ws = w2_scales;
+  p.offsets = offsets;
+  p.out = y;
+  p.M = T * k; p.R = T * k; p.N = H; p.K = I; p.E = E; p.k = k;
+  p.lo = 1; p.hi = INT32_MAX;
+  return launched(contract(mxm::a4::kDown, mxm::a4::kF32, p, as_stream(stream)));
+}
+
+int moe_mxfp4_a4_layer(const uint16_t* x_bf16, const float* logits, int T, int H, int I, int E,
+                       int k, const uint8_t* w13_codes, const uint8_t* w13_scales,
+                       const uint8_t* w2_codes, const uint8_t* w2_scales, int32_t* topk_ids,
+                       float* topk_w, int32_t* counts, int32_t* offsets, int32_t* sorted_pairs,
+                       int32_t* pair_to_row, uint8_t* x_codes, uint8_t* x_scales,
+                       uint8_t* h_codes, uint8_t* h_scales, float* y, float* out,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  // check everything before enqueuing anything
+  int st = check_ffn_shape(T, H, I, E, k);
+  if (st != MXM_OK) return st;
+  const size_t need = moe_permute_workspace_bytes(T, E, k);
+  if (workspace_bytes < need) return MXM_ERR_WORKSPACE;
+  if (T == 0) return MXM_OK;
+  if (!x_bf16 || !logits || !w13_codes || !w13_scales || !w2_codes || !w2_scales || !topk_ids ||
+      !topk_w || !counts || !offsets || !sorted_pairs || !pair_to_row || !x_codes || !x_scales ||
+      !h_codes || !h_scales || !y || !out || (need > 0 && !workspace))
+    return MXM_ERR_NULL;
+  if (!aligned(x_bf16, 16) || !aligned(w13_codes, 16) || !aligned(w2_codes, 16) ||
+      !aligned(x_codes, 16) || !aligned(h_codes, 16) || !aligned(y, 16) || !aligned(out, 16) ||
+      !aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
+      !aligned(counts, 4) || !aligned(offsets, 4) || !aligned(sorted_pairs, 4) ||
+      !aligned(pair_to_row, 4) || !aligned(workspace, 4))
+    return MXM_ERR_ALIGN;
+  if ((st = moe_route_permute(logits, T, E, k, topk_ids, topk_w, counts, offsets, sorted_pairs,
+                              pair_to_row, workspace, workspace_bytes, stream)) != MXM_OK)
+    return st;
+  if ((st = mxfp4_pack(x_bf16, MXM_BF16, T, H, x_codes, x_scales, stream)) != MXM_OK) return st;
+  if ((st = moe_mxfp4_a4_gate_up_swiglu(x_codes, x_scales, sorted_pairs, offsets, T, H, I, E, k,
+                                        w13_codes, w13_scales, nullptr, h_codes, h_scales,
+                                        stream)) != MXM_OK)
+    return st;
+  if ((st = moe_mxfp4_a4_down(h_codes, h_scales, offsets, T, H, I, E, k, w2_codes, w2_scales, y,
+                              stream)) != MXM_OK)
+    return st;
+  return moe_combine(y, topk_w, pair_to_row, T, H, k, out, stream);
+}
+
+size_t dflash_verify_probs_workspace_bytes(int B, int L, int V) {
+  if (B < 1 || L < 1 || L > kMaxVerifyL || V < 1) return 0;
+  return mxm::verify_probs_workspace_bytes(B, V);
+}
+
+int dflash_verify_probs(const void* target_probs, const void* draft_probs, int dtype,
+                        const int32_t* draft_tokens, const int32_t* draft_len,
+                        const float* uniforms, int B, int L, int V, int32_t* accept_len,
+                        int32_t* next_token, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  if (dtype != MXM_F32 && dtype != MXM_BF16) return MXM_ERR_DTYPE;
+  // parts of a block and a row's elements are counted in 31 bits
+  if (B < 0 || B > (1 << 24) || L < 1 || L > kMaxVerifyL || V < 1 || V > (1 << 30))
+    return MXM_ERR_SHAPE;
+  if (B == 0) return MXM_OK;
+  if (workspace_bytes < dflash_verify_probs_workspace_bytes(B, L, V)) return MXM_ERR_WORKSPACE;
+  if (!target_probs || !draft_probs || !draft_tokens || !uniforms || !accept_len || !next_token ||
+      !workspace)
+    return MXM_ERR_NULL;
+  const uintptr_t size = dtype == MXM_F32 ? 4 : 2;
+  if (!aligned(target_probs, size) || !aligned(draft_probs, size) || !aligned(draft_tokens, 4) ||
+      !aligned(draft_len, 4) || !aligned(uniforms, 4) || !aligned(accept_len, 4) ||
+      !aligned(next_token, 4) || !aligned(workspace, 8))
+    return MXM_ERR_ALIGN;
+  return launched(mxm::launch_verify_probs(target_probs, draft_probs, dtype == MXM_BF16,
+                                           draft_tokens, draft_len, uniforms, B, L, V, accept_len,
+                                           next_token, workspace, as_stream(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,251 @@
+// Contractions of two MXFP4 factors without staging: every wave loads its
+// operands from memory straight into the registers of the scaled matrix
+// instructions.  Takes every shape.
+//
+// A workgroup's unit is 16 CF output columns x 16 MS rows over the whole of
+// K.  Its waves deal the 256-element chunks of K among themselves (a chunk is
+// one 128-byte line of codes per row) and their partial sums meet in LDS,
+// added in wave order, so results do not depend on timing.  Splitting K
+// rather than the columns keeps every byte of a unit in flight at once: with
+// few rows the cost is the latency of the weight bytes, not their number.
+#include "a4.hpp"
+#include "mx_pack.hpp"
+
+namespace mxm {
+namespace a4 {
+namespace {
+
+constexpr int kWaves = 8;
+constexpr int kThreads = kWaves * kWave;
+constexpr int kChunkBlocks = 8;                // MX blocks per chunk (256 of K)
+
+template <bool LINES>
+struct Frag {
+  uint4 c[2];            // this lane's blocks g and 4 + g of the chunk
+  uint32_t s[2];         // and their scale bytes
+};
+
+// Chunk `ch` of the row at (codes, scales).  LINES: K is whole chunks and the
+// scale rows are 8-byte aligned.  Blocks past the end of K load as zeros under
+// scale 1: they add nothing, whatever the other factor holds.
+template <bool LINES>
+__device__ __forceinline__ Frag<LINES> load_frag(const uint8_t* codes, const uint8_t* scales,
+                                                 int ch, int nblk) {
+  const int g = lane_id() >> 4;
+  Frag<LINES> f;
+  if constexpr (LINES) {
+    f.c[0] = *reinterpret_cast<const uint4*>(codes + 128 * int64_t(ch) + 16 * g);
+    f.c[1] = *reinterpret_cast<const uint4*>(codes + 128 * int64_t(ch) + 64 + 16 * g);
+    const uint2 s = *reinterpret_cast<const uint2*>(scales + 8 * ch);
+    f.s[0] = s.x >> (8 * g);
+    f.s[1] = s.y >> (8 * g);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int b = kChunkBlocks * ch + 4 * h + g;
+      const int bc = min(b, nblk - 1);
+      f.c[h] = *reinterpret_cast<const uint4*>(codes + 16 * int64_t(bc));
+      f.s[h] = scales[bc];
+      if (b >= nblk) {
+        f.c[h] = make_uint4(0u, 0u, 0u, 0u);
+        f.s[h] = 127u;
+      }
+    }
+  }
+  return f;
+}
+
+// CF: 16-column groups per unit; MS: 16-row groups per unit.
+template <Kind KIND, Out OUT, int CF, int MS, bool LINES>
+__global__ __launch_bounds__(kThreads) void k_direct(Problem p) {
+  constexpr int WF = KIND == kGateUp ? 2 * CF : CF;        // weight fragments
+  __shared__ f32x4 part[kWaves][WF * MS][kWave];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = lane_id();
+  const int r16 = lane & 15, g = lane >> 4;
+  const int nblk = p.K / 32;
+  const int64_t crow = p.K / 2;
+  const int nch = (nblk + kChunkBlocks - 1) / kChunkBlocks;
+  const int ncol = (p.N + 16 * CF - 1) / (16 * CF);
+
+  for (int64_t slot = blockIdx.x;; slot += gridDim.x) {
+    const int tau = int(slot / ncol);
+    const int n0 = int(slot - int64_t(tau) * ncol) * 16 * CF;
+    Tile t;
+    if constexpr (KIND == kGemm) {
+      t.e = 0;
+      t.row0 = tau * 16 * MS;
+      t.rows = min(16 * MS, p.M - t.row0);
+      if (t.rows <= 0) break;
+    } else {
+      if (!find_tile(p.offsets, p.E, 16 * MS, tau, t, p.lo, p.hi)) break;
+    }
+
+    const uint8_t* xc[MS];
+    const uint8_t* xs[MS];
+#pragma unroll
+    for (int m = 0; m < MS; ++m) {
+      int64_t row = t.row0 + min(16 * m + r16, t.rows - 1);
+      if constexpr (KIND == kGateUp) row = p.pairs[row] / p.k;
+      xc[m] = p.xc + row * crow;
+      xs[m] = p.xs + row * nblk;
+    }
+    const uint8_t* wc[WF];
+    const uint8_t* ws[WF];
+#pragma unroll
+    for (int a = 0; a < WF; ++a) {
+      const int n = min(n0 + 16 * (a % CF) + r16, p.N - 1);
+      const int64_t row = KIND == kGateUp ? (int64_t(t.e) * 2 + a / CF) * p.N + n
+                                          : int64_t(t.e) * p.N + n;
+      wc[a] = p.wc + row * crow;
+      ws[a] = p.ws + row * nblk;
+    }
+
+    f32x4 acc[WF][MS];
+#pragma unroll
+    for (int a = 0; a < WF; ++a)
+#pragma unroll
+      for (int m = 0; m < MS; ++m) acc[a][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int ch = wave; ch < nch; ch += kWaves) {
+      Frag<LINES> w[WF], x[MS];
+#pragma unroll
+      for (int a = 0; a < WF; ++a) w[a] = load_frag<LINES>(wc[a], ws[a], ch, nblk);
+#pragma unroll
+      for (int m = 0; m < MS; ++m) x[m] = load_frag<LINES>(xc[m], xs[m], ch, nblk);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int a = 0; a < WF; ++a)
+#pragma unroll
+          for (int m = 0; m < MS; ++m)
+            acc[a][m] = mfma(w[a].c[h], w[a].s[h], x[m].c[h], x[m].s[h], acc[a][m]);
+    }
+#pragma unroll
+    for (int a = 0; a < WF; ++a)
+#pragma unroll
+      for (int m = 0; m < MS; ++m) part[wave][a * MS + m][lane] = acc[a][m];
+    __syncthreads();
+
+    // the row groups' sums are dealt over the waves; lane: columns 4g .. 4g+3
+    // of row r16
+    auto total = [&](int a, int m) {
+      f32x4 v = part[0][a * MS + m][lane];
+#pragma unroll
+      for (int q = 1; q < kWaves; ++q) v += part[q][a * MS + m][lane];
+      return v;
+    };
+    for (int m = wave; m < MS; m += kWaves) {
+      const int64_t row = int64_t(t.row0) + 16 * m + r16;
+      const bool live = 16 * m + r16 < t.rows;
+      if constexpr (OUT == kMx) {
+        static_assert(OUT != kMx || CF == 2, "an MX block is two 16-column groups");
+        // h rounded to bf16, then packed: the block's 32 columns are this
+        // lane's eight and those of lanes +-16, +-32
+        uint32_t v[2][4];
+        uint32_t amax = 0;
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const f32x4 gv = total(a, m), uv = total(a + CF, m);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[a][i] = f32_to_bf16_rne(silu_mul(gv[i], uv[i])) << 16;
+            amax = max(amax, v[a][i] & 0x7fffffffu);
+          }
+        }
+        amax = max(amax, uint32_t(__shfl_xor(int(amax), 16)));
+        amax = max(amax, uint32_t(__shfl_xor(int(amax), 32)));
+        const bool bad = amax >= 0x7f800000u;            // Inf or NaN in the block
+        const uint32_t e = bad ? 255u : mx_scale_byte(amax);
+        const MxThresholds th(bad ? 0u : e);
+        if (live) {
+          uint8_t* oc = p.oc + row * (p.N / 2) + n0 / 2;
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            uint32_t c = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c |= th.code(v[a][i]) << (4 * i);
+            *reinterpret_cast<uint16_t*>(oc + 8 * a + 2 * g) = uint16_t(bad ? 0u : c);
+          }
+          if (g == 0) p.os[row * (p.N / 32) + n0 / 32] = uint8_t(e);
+        }
+      } else {
+#pragma unroll
+        for (int a = 0; a < CF; ++a) {
+          f32x4 v = total(a, m);
+          if constexpr (KIND == kGateUp) {
+            const f32x4 u = total(a + CF, m);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = silu_mul(v[i], u[i]);
+          }
+          if (!live) continue;
+          const int n = n0 + 16 * a + 4 * g;
+          // rows of 4 n columns start on whole 16 (8) bytes; others are
+          // written one by one
+          if constexpr (OUT == kF32) {
+            float* o = static_cast<float*>(p.out) + row * p.N + n;
+            if (n + 4 <= p.N && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+              *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (n + i < p.N) o[i] = v[i];
+            }
+          } else {
+            uint16_t* o = static_cast<uint16_t*>(p.out) + row * p.N + n;
+            uint32_t b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = f32_to_bf16_rne(v[i]);
+            if (n + 4 <= p.N && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+              *reinterpret_cast<uint2*>(o) = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (n + i < p.N) o[i] = uint16_t(b[i]);
+            }
+          }
+        }
+      }
+    }
+    __syncthreads();                 // the sums are read: LDS is free
+  }
+}
+
+template <Kind KIND, Out OUT, int CF, int MS>
+hipError_t launch(const Problem& p, hipStream_t s) {
+  const bool lines = p.K % 256 == 0 && reinterpret_cast<uintptr_t>(p.xs) % 8 == 0 &&
+                     reinterpret_cast<uintptr_t>(p.ws) % 8 == 0;
+  const int64_t ncol = (p.N + 16 * CF - 1) / (16 * CF);
+  // row tiles: exact for a product, at most one partial tile per expert else
+  const int64_t full = p.R / (16 * MS);
+  const int64_t tiles = KIND == kGemm ? (int64_t(p.M) + 16 * MS - 1) / (16 * MS)
+                                      : full + (p.R < p.E ? p.R : p.E);
+  const int64_t cap = int64_t(device_cus()) * 4;
+  const int64_t slots = tiles * ncol;
+  const unsigned grid = unsigned(slots < cap ? slots : cap);
+  if (lines) k_direct<KIND, OUT, CF, MS, true><<<grid, kThreads, 0, s>>>(p);
+  else k_direct<KIND, OUT, CF, MS, false><<<grid, kThreads, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+template <Kind KIND, Out OUT, int CF>
+hipError_t launch_rows(const Problem& p, hipStream_t s) {
+  const int groups = KIND == kGemm || p.R < p.E ? 1 : p.E;
+  const int mean = (KIND == kGemm ? p.M : p.R) / groups;
+  if (mean <= 16) return launch<KIND, OUT, CF, 1>(p, s);
+  return launch<KIND, OUT, CF, 4>(p, s);
+}
+
+}  // namespace
+
+hipError_t launch_direct(Kind kind, Out out, const Problem& p, hipStream_t s) {
+  if (kind == kGemm) {
+    if (out == kBf16) return launch_rows<kGemm, kBf16, 1>(p, s);
+    return launch_rows<kGemm, kF32, 1>(p, s);
+  }
+  if (kind == kDown) return launch_rows<kDown, kF32, 1>(p, s);
+  if (out == kMx) return launch<kGateUp, kMx, 2, 1>(p, s);
+  return launch_rows<kGateUp, kBf16, 1>(p, s);
+}
+
+}  // namespace a4
+}  // namespace mxm

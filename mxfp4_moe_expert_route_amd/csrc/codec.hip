@@ -8,7 +8,7 @@
 // Both directions build IEEE bit patterns with integer arithmetic, so results
 // are exact (subnormal inputs and outputs included) and independent of the
 // floating-point denormal mode.  One thread handles one 32-element block.
-#include "common.hpp"
+#include "mx_pack.hpp"
 
 namespace mxm {
 namespace {
@@ -67,14 +67,6 @@ __global__ __launch_bounds__(256) void k_unpack(const uint8_t* __restrict__ code
   }
 }
 
-// fp32 bits of (1 + mf/2^23) * 2^p * 2^(e-127) for the rounding midpoints;
-// exact for every e the conversion can choose (see the caller).
-__device__ __forceinline__ uint32_t midpoint_bits(int p, uint32_t mf, int e) {
-  const int be = p + e;
-  if (be >= 1) return (uint32_t(be) << 23) | mf;
-  return (0x800000u | mf) >> (1 - be);               // be >= -2: exact shift
-}
-
 __global__ __launch_bounds__(256) void k_pack(const void* __restrict__ x, int x_bf16,
                                               int64_t nblocks, uint8_t* __restrict__ codes,
                                               uint8_t* __restrict__ scales) {
@@ -114,30 +106,10 @@ __global__ __launch_bounds__(256) void k_pack(const void* __restrict__ x, int x_
     if (bad) {
       e = 255;
     } else {
-      if (amax != 0u) {
-        const int ef = int(amax >> 23);
-        const int fl = ef > 0 ? ef - 127 : (31 - __clz(amax)) - 149;   // floor(log2 amax)
-        e = uint32_t(min(max(fl - 2 + 127, 0), 254));
-      }
-      // E2M1 magnitude code = number of midpoints passed; at a midpoint the
-      // even code wins: strict '>' below an even code, '>=' below an odd one.
-      const int ei = int(e);
-      const uint32_t t0 = midpoint_bits(-2, 0x000000u, ei);   // 0.25
-      const uint32_t t1 = midpoint_bits(-1, 0x400000u, ei);   // 0.75
-      const uint32_t t2 = midpoint_bits(0, 0x200000u, ei);    // 1.25
-      const uint32_t t3 = midpoint_bits(0, 0x600000u, ei);    // 1.75
-      const uint32_t t4 = midpoint_bits(1, 0x200000u, ei);    // 2.5
-      const uint32_t t5 = midpoint_bits(1, 0x600000u, ei);    // 3.5
-      const uint32_t t6 = midpoint_bits(2, 0x200000u, ei);    // 5
+      e = mx_scale_byte(amax);
+      const MxThresholds th(e);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const uint32_t a = v[i] & 0x7fffffffu;
-        uint32_t c = uint32_t(a > t0) + uint32_t(a >= t1) + uint32_t(a > t2) +
-                     uint32_t(a >= t3) + uint32_t(a > t4) + uint32_t(a >= t5) +
-                     uint32_t(a > t6);
-        c |= (v[i] >> 28) & 8u;                      // sign bit of the input
-        out[i >> 3] |= c << (4 * (i & 7));
-      }
+      for (int i = 0; i < 32; ++i) out[i >> 3] |= th.code(v[i]) << (4 * (i & 7));
     }
     *reinterpret_cast<uint4*>(codes + b * 16) = make_uint4(out[0], out[1], out[2], out[3]);
     scales[b] = uint8_t(e);

@@ -340,6 +340,176 @@ def moe_mxfp4_layer_noalloc(x, logits, k, w13_codes, w13_scales, w2_codes, w2_sc
     return b
 
 
+# ---- MXFP4 activations, and verification from probabilities ----------------
+
+def _enqueue(name, device, *args):
+    """Call the library on `device`'s current stream (whatever device is current)."""
+    if device.index == torch.cuda.current_device():
+        check(getattr(lib(), name)(*args, _stream()), name)
+    else:
+        with torch.cuda.device(device):
+            check(getattr(lib(), name)(*args, _stream()), name)
+
+
+def _need_mx(codes, scales, name, shape, device):
+    """codes uint8 [*shape[:-1], K/2] and scales uint8 [*shape[:-1], K/32] of an MXFP4 tensor."""
+    _need(codes, name + "_codes", torch.uint8, (*shape[:-1], shape[-1] // 2), device)
+    _need(scales, name + "_scales", torch.uint8, (*shape[:-1], shape[-1] // 32), device)
+
+
+def _rank(t, name, n):
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise ValueError("%s must be a tensor of %d dimensions" % (name, n))
+    return t.shape
+
+
+def mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, dtype=torch.float32, out=None):
+    """MXFP4 a [M, K] and b [N, K] (codes [rows, K/2], scales [rows, K/32]) ->
+    a b^T [M, N] float32 or bfloat16."""
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("dtype must be float32 or bfloat16")
+    M, half = _rank(a_codes, "a_codes", 2)
+    N, _ = _rank(b_codes, "b_codes", 2)
+    K, dev = 2 * half, a_codes.device
+    _need_mx(a_codes, a_scales, "a", (M, K), dev)
+    _need_mx(b_codes, b_scales, "b", (N, K), dev)
+    out = _out(out, "out", dtype, (M, N), dev)
+    _enqueue("mxfp4_gemm", dev, _ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), M, N,
+             K, _ptr(out), BF16 if dtype == torch.bfloat16 else F32)
+    return out
+
+
+def _a4_gate_up_shapes(x_codes, x_scales, sorted_pairs, offsets, k, w13_codes, w13_scales):
+    T, half = _rank(x_codes, "x_codes", 2)
+    E, two_i, _ = _rank(w13_codes, "w13_codes", 3)
+    H, I, dev = 2 * half, two_i // 2, x_codes.device
+    _need_mx(x_codes, x_scales, "x", (T, H), dev)
+    _need_mx(w13_codes, w13_scales, "w13", (E, 2 * I, H), dev)
+    _need(sorted_pairs, "sorted_pairs", torch.int32, (T * k,), dev)
+    _need(offsets, "offsets", torch.int32, (E + 1,), dev)
+    return T, H, I, E, dev
+
+
+def moe_mxfp4_a4_gate_up_swiglu(x_codes, x_scales, sorted_pairs, offsets, k, w13_codes, w13_scales,
+                                h=None):
+    """MXFP4 x [T, H] -> h [T*k, I] bfloat16 (rows in sorted order)."""
+    T, H, I, E, dev = _a4_gate_up_shapes(x_codes, x_scales, sorted_pairs, offsets, k, w13_codes,
+                                         w13_scales)
+    h = _out(h, "h", torch.bfloat16, (T * k, I), dev)
+    _enqueue("moe_mxfp4_a4_gate_up_swiglu", dev, _ptr(x_codes), _ptr(x_scales), _ptr(sorted_pairs),
+             _ptr(offsets), T, H, I, E, k, _ptr(w13_codes), _ptr(w13_scales), _ptr(h), None, None)
+    return h
+
+
+def moe_mxfp4_a4_gate_up_swiglu_pack(x_codes, x_scales, sorted_pairs, offsets, k, w13_codes,
+                                     w13_scales, h_codes=None, h_scales=None):
+    """moe_mxfp4_a4_gate_up_swiglu writing h in MXFP4 (mxfp4_pack of the
+    bfloat16 h, bit for bit) -> (h_codes [T*k, I/2], h_scales [T*k, I/32])."""
+    T, H, I, E, dev = _a4_gate_up_shapes(x_codes, x_scales, sorted_pairs, offsets, k, w13_codes,
+                                         w13_scales)
+    h_codes = _out(h_codes, "h_codes", torch.uint8, (T * k, I // 2), dev)
+    h_scales = _out(h_scales, "h_scales", torch.uint8, (T * k, I // 32), dev)
+    _enqueue("moe_mxfp4_a4_gate_up_swiglu", dev, _ptr(x_codes), _ptr(x_scales), _ptr(sorted_pairs),
+             _ptr(offsets), T, H, I, E, k, _ptr(w13_codes), _ptr(w13_scales), None, _ptr(h_codes),
+             _ptr(h_scales))
+    return h_codes, h_scales
+
+
+def moe_mxfp4_a4_down(h_codes, h_scales, offsets, k, w2_codes, w2_scales, y=None):
+    """MXFP4 h [T*k, I] -> y [T*k, H] float32 (rows in sorted order)."""
+    R, half = _rank(h_codes, "h_codes", 2)
+    E, H, _ = _rank(w2_codes, "w2_codes", 3)
+    I, dev = 2 * half, h_codes.device
+    if k < 1 or R % k:
+        raise ValueError("h must have T*k rows")
+    _need_mx(h_codes, h_scales, "h", (R, I), dev)
+    _need_mx(w2_codes, w2_scales, "w2", (E, H, I), dev)
+    _need(offsets, "offsets", torch.int32, (E + 1,), dev)
+    y = _out(y, "y", torch.float32, (R, H), dev)
+    _enqueue("moe_mxfp4_a4_down", dev, _ptr(h_codes), _ptr(h_scales), _ptr(offsets), R // k, H, I,
+             E, k, _ptr(w2_codes), _ptr(w2_scales), _ptr(y))
+    return y
+
+
+class A4LayerBuffers:
+    """Preallocated intermediates of one moe_mxfp4_a4_layer call."""
+
+    def __init__(self, T, H, I, E, k, device):
+        R = T * k
+        z = dict(device=device)
+        self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
+        self.topk_ids = torch.empty((T, k), dtype=torch.int32, **z)
+        self.topk_w = torch.empty((T, k), dtype=torch.float32, **z)
+        self.counts = torch.empty((E,), dtype=torch.int32, **z)
+        self.offsets = torch.empty((E + 1,), dtype=torch.int32, **z)
+        self.sorted_pairs = torch.empty((R,), dtype=torch.int32, **z)
+        self.pair_to_row = torch.empty((R,), dtype=torch.int32, **z)
+        self.x_codes = torch.empty((T, H // 2), dtype=torch.uint8, **z)
+        self.x_scales = torch.empty((T, H // 32), dtype=torch.uint8, **z)
+        self.h_codes = torch.empty((R, I // 2), dtype=torch.uint8, **z)
+        self.h_scales = torch.empty((R, I // 32), dtype=torch.uint8, **z)
+        self.y = torch.empty((R, H), dtype=torch.float32, **z)
+        self.out = torch.empty((T, H), dtype=torch.float32, **z)
+        nws = moe_permute_workspace_bytes(T, E, k)
+        self.workspace = torch.empty(max(nws, 1), dtype=torch.uint8, **z)
+
+
+def moe_mxfp4_a4_layer(x, logits, k, w13_codes, w13_scales, w2_codes, w2_scales, buffers=None):
+    """The whole layer with MXFP4 activations in one C call (route, permute,
+    pack x, gate/up with h in MXFP4, down, combine).
+
+    Returns the A4LayerBuffers holding every intermediate; `.out` is the result."""
+    T, H = _rank(x, "x", 2)
+    E, two_i, _ = _rank(w13_codes, "w13_codes", 3)
+    I, dev = two_i // 2, x.device
+    _need(x, "x", torch.bfloat16)
+    _need(logits, "logits", torch.float32, (T, E), dev)
+    _need_mx(w13_codes, w13_scales, "w13", (E, 2 * I, H), dev)
+    _need_mx(w2_codes, w2_scales, "w2", (E, H, I), dev)
+    b = buffers if buffers is not None else A4LayerBuffers(T, H, I, E, k, dev)
+    if (b.T, b.H, b.I, b.E, b.k) != (T, H, I, E, k) or b.out.device != dev:
+        raise ValueError("buffers were made for another shape or device")
+    _enqueue("moe_mxfp4_a4_layer", dev, _ptr(x), _ptr(logits), T, H, I, E, k, _ptr(w13_codes),
+             _ptr(w13_scales), _ptr(w2_codes), _ptr(w2_scales), _ptr(b.topk_ids), _ptr(b.topk_w),
+             _ptr(b.counts), _ptr(b.offsets), _ptr(b.sorted_pairs), _ptr(b.pair_to_row),
+             _ptr(b.x_codes), _ptr(b.x_scales), _ptr(b.h_codes), _ptr(b.h_scales), _ptr(b.y),
+             _ptr(b.out), _ptr(b.workspace), b.workspace.numel())
+    return b
+
+
+def dflash_verify_probs_workspace_bytes(B, L, V):
+    return int(lib().dflash_verify_probs_workspace_bytes(B, L, V))
+
+
+def dflash_verify_probs(target_probs, draft_probs, draft_tokens, uniforms, draft_len=None,
+                        accept_len=None, next_token=None, workspace=None):
+    """target_probs [B, L+1, V], draft_probs [B, L, V] (both float32 or both
+    bfloat16), draft_tokens [B, L] int32, uniforms [B, L+1] f32, draft_len [B]
+    int32 or None (every block has L tokens) -> (accept_len int32 [B],
+    next_token int32 [B], -1 where no token has probability)."""
+    B, L, V = _rank(draft_probs, "draft_probs", 3)
+    dev, dtype = draft_probs.device, draft_probs.dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("draft_probs must be float32 or bfloat16")
+    _need(draft_probs, "draft_probs", dtype)
+    _need(target_probs, "target_probs", dtype, (B, L + 1, V), dev)
+    _need(draft_tokens, "draft_tokens", torch.int32, (B, L), dev)
+    _need(uniforms, "uniforms", torch.float32, (B, L + 1), dev)
+    if draft_len is not None:
+        _need(draft_len, "draft_len", torch.int32, (B,), dev)
+    accept_len = _out(accept_len, "accept_len", torch.int32, (B,), dev)
+    next_token = _out(next_token, "next_token", torch.int32, (B,), dev)
+    if workspace is None:
+        workspace = torch.empty(max(dflash_verify_probs_workspace_bytes(B, L, V), 8),
+                                dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, None, dev)
+    _enqueue("dflash_verify_probs", dev, _ptr(target_probs), _ptr(draft_probs),
+             BF16 if dtype == torch.bfloat16 else F32, _ptr(draft_tokens), _ptr(draft_len),
+             _ptr(uniforms), B, L, V, _ptr(accept_len), _ptr(next_token), _ptr(workspace),
+             workspace.numel())
+    return accept_len, next_token
+
+
 def mxm_stream_xor(src, result, nontemporal=False):
     """Streaming-read probe (a measurement aid): XOR every 32-bit word of the
     contiguous tensor `src` (byte size a multiple of 16) into `result`, an
