@@ -60,7 +60,11 @@ struct Problem {
   int lo, hi;
 };
 
+// Operands straight from memory: every shape.
 hipError_t launch_direct(Kind kind, Out out, const Problem& p, hipStream_t s);
+// Persistent, through LDS.
+bool tiled_supported(Kind kind, const Problem& p);
+hipError_t launch_tiled(Kind kind, Out out, const Problem& p, hipStream_t s);
 
 }  // namespace a4
 

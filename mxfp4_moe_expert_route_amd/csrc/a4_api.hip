@@ -31,6 +31,8 @@ int check_ffn_shape(int T, int H, int I, int E, int k) {
 
 // Where the contraction runs (decided from sizes alone).
 hipError_t contract(mxm::a4::Kind kind, mxm::a4::Out out, const Problem& p, hipStream_t s) {
+  if (mxm::a4::tiled_supported(kind, p) && (kind != mxm::a4::kGemm || p.M > 16))
+    return mxm::a4::launch_tiled(kind, out, p, s);
   return mxm::a4::launch_direct(kind, out, p, s);
 }
 
