@@ -422,7 +422,8 @@ int moe_mxfp4_a4_layer(const uint16_t* x_bf16, const float* logits, int T, int H
                        uint8_t* h_codes, uint8_t* h_scales, float* y, float* out,
                        void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace dflash_verify_probs needs (0 for invalid sizes). */
+/* Workspace dflash_verify_probs needs: 0 where one launch does it all (small
+ * vocabularies, large batches) and for invalid sizes. */
 size_t dflash_verify_probs_workspace_bytes(int B, int L, int V);
 
 /*
@@ -439,8 +440,8 @@ size_t dflash_verify_probs_workspace_bytes(int B, int L, int V);
  *   accept_len   [B] int32, written: n, the leading positions accepted
  *   next_token   [B] int32, written: the token after the n accepted ones
  *   workspace    dflash_verify_probs_workspace_bytes(B, L, V) bytes, 8-byte
- *                aligned; its contents need no initialisation.  Calls that
- *                share one must not overlap.
+ *                aligned (may be NULL when that is 0); its contents need no
+ *                initialisation.  Calls that share one must not overlap.
  * Rule of dflash_verify_accept with p_i = target_probs[b, i] and q_i =
  * draft_probs[b, i] as given: they need not sum to 1, and an entry that is
  * not a positive finite number counts as 0.  After a whole block

@@ -152,9 +152,10 @@ int dflash_verify_probs(const void* target_probs, const void* draft_probs, int d
   if (B < 0 || B > (1 << 24) || L < 1 || L > kMaxVerifyL || V < 1 || V > (1 << 30))
     return MXM_ERR_SHAPE;
   if (B == 0) return MXM_OK;
-  if (workspace_bytes < dflash_verify_probs_workspace_bytes(B, L, V)) return MXM_ERR_WORKSPACE;
+  const size_t need = dflash_verify_probs_workspace_bytes(B, L, V);
+  if (workspace_bytes < need) return MXM_ERR_WORKSPACE;
   if (!target_probs || !draft_probs || !draft_tokens || !uniforms || !accept_len || !next_token ||
-      !workspace)
+      (need > 0 && !workspace))
     return MXM_ERR_NULL;
   const uintptr_t size = dtype == MXM_F32 ? 4 : 2;
   if (!aligned(target_probs, size) || !aligned(draft_probs, size) || !aligned(draft_tokens, 4) ||

@@ -9,35 +9,46 @@
 // sum of weights exceeds u_L times their sum.
 //
 // Decisions are made in fp64: products and differences of two fp32 (or bf16)
-// values are exact there, and a sum over a vocabulary of 2^18 is off by at
-// most 2^-35 of itself, so a draw depends on the order of summation only
-// where u_L falls within that of a boundary.  Sums run in a fixed order.
+// values are exact there (differences up to 2^-53 of the larger), and a sum
+// over a vocabulary of 2^18 is off by at most 2^-35 of itself, so a draw
+// depends on the order of summation only where u_L falls within that of a
+// boundary.  Sums run in a fixed order.
 //
 // Of the (L + 1) V probabilities of a block only the drafted tokens' entries
-// and the two rows at position n are read.  Two launches: the weights' sums
-// over parts of row n, by workgroups that each find n themselves (2 L loads,
-// cheaper than a launch), then one workgroup per block that finds the part
-// holding the draw and reads it again.
+// and the two rows at position n are read.  A row is cut into parts, one
+// wave's sum each; the draw finds the part that holds it and reads that one
+// again.  A small vocabulary (or a batch that fills the CUs by itself) takes
+// one launch, a workgroup per block.  A large one takes two, since fp64 sums
+// over 152064 tokens keep one CU busy for about 16 us: the parts' sums by
+// workgroups that each find n themselves (2 L loads, cheaper than a launch),
+// then the draw.
 #include "a4.hpp"
 
 namespace mxm {
 namespace {
 
-constexpr int kT = 256;
-constexpr int kWavesV = kT / kWave;
-constexpr int kMaxParts = 128;
-constexpr int kMinPart = 4 * kT;               // elements a part is worth a workgroup for
+constexpr int kSplitT = 256;                   // threads of a summing workgroup
+constexpr int kDrawT = 512;
+constexpr int kOneT = 1024;                    // threads where one workgroup does it all
+constexpr int kMaxParts = 256;
+constexpr int kOneV = 16384;                   // vocabulary one workgroup sums in about 2 us
+constexpr int kOneB = 512;                     // blocks that fill the CUs by themselves
 
-struct Sums {
-  double w, p;                                 // of max(0, p - q), of p
-};
+bool one_launch(int B, int V) { return V <= kOneV || B >= kOneB; }
 
-// Parts per row: enough workgroups to fill the CUs, none below kMinPart.
+// Parts per row where two launches are taken: about eight waves a CU, at
+// least 512 tokens a wave.
 int parts_of(int B, int V) {
-  int n = (4 * 256 + B - 1) / B;
-  const int most = (V + kMinPart - 1) / kMinPart;
+  int n = 2048 / B;
+  const int most = (V + 511) / 512;
   n = n < most ? n : most;
-  return n < 1 ? 1 : (n > kMaxParts ? kMaxParts : n);
+  n = n < kMaxParts ? n : kMaxParts;
+  return n < 4 ? 4 : n / 4 * 4;                // whole summing workgroups
+}
+
+// Elements per part: whole 16-byte vectors of either type.
+__host__ __device__ __forceinline__ int span_of(int V, int parts) {
+  return ((V + parts - 1) / parts + 7) & ~7;
 }
 
 __device__ __forceinline__ float value(const float* p, int64_t i) { return p[i]; }
@@ -46,8 +57,13 @@ __device__ __forceinline__ float value(const uint16_t* p, int64_t i) {
 }
 
 // A probability: what is not a positive finite number counts as none.
-__device__ __forceinline__ double clean(float v) {
-  return v > 0.f && v < INFINITY ? double(v) : 0.0;
+__device__ __forceinline__ float clean(float v) {
+  return __float_as_uint(v) - 1u < 0x7f7fffffu ? v : 0.f;
+}
+
+// max(0, p - q), or p (q = 0)
+__device__ __forceinline__ double weight(float p, float q) {
+  return fmax(double(clean(p)) - double(clean(q)), 0.0);
 }
 
 __device__ __forceinline__ double wave_sum(double v) {
@@ -56,194 +72,286 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-// Accepted tokens of block b (every wave computes it; uniform result).
-template <typename T>
-__device__ __forceinline__ int accepted(const T* target, const T* draft, const int32_t* tokens,
-                                        const float* uniforms, int len, int b, int L, int V) {
-  const int lane = lane_id();
-  bool fail = false;
-  if (lane < len) {
-    const int64_t at = int64_t(b) * L + lane;
-    const int d = tokens[at];
-    fail = true;
-    if (d >= 0 && d < V) {
-      const double pd = clean(value(target, (at + b) * V + d));
-      const double qd = clean(value(draft, at * V + d));
-      fail = !(double(uniforms[at + b]) * qd < pd);
-    }
+// W consecutive values from element i (a multiple of W of an aligned row).
+template <int W>
+__device__ __forceinline__ void load(const float* p, int i, float (&v)[W]) {
+  if constexpr (W == 1) {
+    v[0] = p[i];
+  } else {
+    const float4 x = *reinterpret_cast<const float4*>(p + i);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
   }
-  const unsigned long long m = __ballot(fail);
-  return __builtin_amdgcn_readfirstlane(m ? __ffsll((long long)m) - 1 : len);
 }
-
-__device__ __forceinline__ int block_len(const int32_t* draft_len, int b, int L) {
-  return draft_len ? min(max(draft_len[b], 0), L) : L;
-}
-
-template <typename T>
-__global__ __launch_bounds__(kT) void k_vp_sums(const T* __restrict__ target,
-                                                const T* __restrict__ draft,
-                                                const int32_t* __restrict__ tokens,
-                                                const int32_t* __restrict__ draft_len,
-                                                const float* __restrict__ uniforms, int L, int V,
-                                                int span, int parts, Sums* __restrict__ sums,
-                                                int32_t* __restrict__ accept_len) {
-  __shared__ Sums ws[kWavesV];
-  const int b = blockIdx.x / parts, part = blockIdx.x - b * parts, tid = threadIdx.x;
-  const int len = block_len(draft_len, b, L);
-  const int n = accepted(target, draft, tokens, uniforms, len, b, L, V);
-  const bool residual = n < len;
-  const T* p = target + (int64_t(b) * (L + 1) + n) * V;
-  const T* q = draft + (int64_t(b) * L + (residual ? n : 0)) * V;
-  const int v0 = part * span, v1 = min(v0 + span, V);
-  double sw = 0.0, sp = 0.0;
-  for (int v = v0 + tid; v < v1; v += kT) {
-    const double pv = clean(value(p, v));
-    const double qv = residual ? clean(value(q, v)) : 0.0;
-    sp += pv;
-    sw += pv > qv ? pv - qv : 0.0;
-  }
-  sw = wave_sum(sw);
-  sp = wave_sum(sp);
-  if (lane_id() == 0) ws[tid / kWave] = Sums{sw, sp};
-  __syncthreads();
-  if (tid == 0) {
-    Sums t = ws[0];
+template <int W>
+__device__ __forceinline__ void load(const uint16_t* p, int i, float (&v)[W]) {
+  if constexpr (W == 1) {
+    v[0] = value(p, i);
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4*>(p + i);
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int w = 1; w < kWavesV; ++w) {
-      t.w += ws[w].w;
-      t.p += ws[w].p;
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(u[k] << 16);
+      v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
     }
-    sums[blockIdx.x] = t;
+  }
+}
+
+// One wave's sum of the weights of tokens v0 .. v1 - 1; q may be NULL (0).
+// Loads of a round are issued together: a part's time is their latency.
+template <int W, class T>
+__device__ __forceinline__ double part_sum(const T* p, const T* q, int v0, int v1) {
+  constexpr int kU = W == 1 ? 8 : 3;
+  double s = 0.0;
+  for (int base = v0; base < v1; base += kWave * W * kU) {
+    float pv[kU][W], qv[kU][W];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int i = base + (u * kWave + lane_id()) * W;
+#pragma unroll
+      for (int k = 0; k < W; ++k) pv[u][k] = qv[u][k] = 0.f;
+      if (i < v1) {
+        load<W>(p, i, pv[u]);
+        if (q) load<W>(q, i, qv[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int k = 0; k < W; ++k) s += weight(pv[u][k], qv[u][k]);
+  }
+  return wave_sum(s);
+}
+
+// The same, by whole vectors where the rows allow it (V a multiple of 8 for
+// bf16, 4 for fp32, and aligned tensors: then every row and part is).
+template <class T>
+__device__ __forceinline__ double part_sum(const T* p, const T* q, int v0, int v1, bool vec) {
+  return vec ? part_sum<16 / int(sizeof(T))>(p, q, v0, v1) : part_sum<1>(p, q, v0, v1);
+}
+
+// One block's inputs.
+template <class T>
+struct Block {
+  const T* target;                             // [L+1, V]
+  const T* draft;                              // [L, V]
+  const int32_t* tokens;
+  const float* u;
+  int len, L, V;
+
+  __device__ __forceinline__ Block(const T* t, const T* d, const int32_t* tok,
+                                   const int32_t* draft_len, const float* uni, int b, int L_, int V_)
+      : target(t + int64_t(b) * (L_ + 1) * V_), draft(d + int64_t(b) * L_ * V_),
+        tokens(tok + int64_t(b) * L_), u(uni + int64_t(b) * (L_ + 1)),
+        len(draft_len ? min(max(draft_len[b], 0), L_) : L_), L(L_), V(V_) {}
+
+  // Accepted tokens (every wave computes it; uniform result).
+  __device__ __forceinline__ int accepted() const {
+    const int lane = lane_id();
+    bool fail = false;
+    if (lane < len) {
+      const int d = tokens[lane];
+      fail = true;
+      if (d >= 0 && d < V) {
+        const double pd = clean(value(target, int64_t(lane) * V + d));
+        const double qd = clean(value(draft, int64_t(lane) * V + d));
+        fail = !(double(u[lane]) * qd < pd);
+      }
+    }
+    const unsigned long long m = __ballot(fail);
+    return __builtin_amdgcn_readfirstlane(m ? __ffsll((long long)m) - 1 : len);
+  }
+  __device__ __forceinline__ const T* p(int n) const { return target + int64_t(n) * V; }
+  __device__ __forceinline__ const T* q(int n) const {
+    return n < len ? draft + int64_t(n) * V : nullptr;
+  }
+};
+
+// Inclusive prefix sum over the workgroup's threads; tot: one double per wave.
+template <int NT>
+__device__ __forceinline__ double block_prefix(double v, double* tot) {
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const double o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  __syncthreads();                             // tot is free
+  if (lane == kWave - 1) tot[wave] = v;
+  __syncthreads();
+  double before = 0.0;
+#pragma unroll
+  for (int w = 0; w < NT / kWave; ++w)
+    if (w < wave) before += tot[w];
+  return before + v;
+}
+
+// The first thread for which `hit`, failing that the last for which `pos`
+// (a goal rounded onto the total), failing that -1.
+template <int NT>
+__device__ __forceinline__ int claim(bool hit, bool pos, unsigned long long* m) {
+  constexpr int kW = NT / kWave;
+  const unsigned long long h = __ballot(hit), p = __ballot(pos);
+  __syncthreads();
+  if (lane_id() == 0) {
+    m[threadIdx.x / kWave] = h;
+    m[kW + threadIdx.x / kWave] = p;
+  }
+  __syncthreads();
+  int c = -1;
+#pragma unroll
+  for (int w = kW - 1; w >= 0; --w)
+    if (m[w]) c = w * kWave + __ffsll((long long)m[w]) - 1;
+  if (c >= 0) return c;
+#pragma unroll
+  for (int w = 0; w < kW; ++w)
+    if (m[kW + w]) c = w * kWave + 63 - __clzll((long long)m[kW + w]);
+  return c;
+}
+
+template <int NT>
+struct DrawLds {
+  double sum[kMaxParts];
+  double tot[NT / kWave];
+  unsigned long long mask[2 * (NT / kWave)];
+  double base;
+};
+
+// The draw from max(0, p - q), the sums of its parts given in s.sum.
+template <int NT, class T>
+__device__ __forceinline__ int draw(const T* p, const T* q, int V, int parts, int span, float u,
+                                    bool vec, DrawLds<NT>& s) {
+  static_assert(NT >= kMaxParts, "one thread per part");
+  const int tid = threadIdx.x;
+  for (;;) {
+    const double own = tid < parts ? s.sum[tid] : 0.0;
+    const double incl = block_prefix<NT>(own, s.tot);
+    double total = 0.0;
+#pragma unroll
+    for (int w = 0; w < NT / kWave; ++w) total += s.tot[w];
+    if (!(total > 0.0)) {
+      if (!q) return -1;                       // no token has probability
+      q = nullptr;                             // no difference: from p itself
+      __syncthreads();
+      for (int k = tid / kWave; k < parts; k += NT / kWave) {
+        const double t = part_sum(p, q, min(k * span, V), min((k + 1) * span, V), vec);
+        if (lane_id() == 0) s.sum[k] = t;
+      }
+      __syncthreads();
+      continue;
+    }
+    const double goal = double(u) * total;
+    const int part = claim<NT>(own > 0.0 && goal < incl, own > 0.0, s.mask);
+    if (tid == part) s.base = incl - own;
+    __syncthreads();
+    const double base = s.base;
+    // thread t owns a run of `each` tokens, so thread order is token order
+    const int v0 = min(part * span, V), v1 = min(v0 + span, V);
+    const int each = (v1 - v0 + NT - 1) / NT;
+    const int a0 = min(v0 + tid * each, v1), a1 = min(a0 + each, v1);
+    double run = 0.0;
+    for (int v = a0; v < a1; ++v) run += weight(value(p, v), q ? value(q, v) : 0.f);
+    const double end = base + block_prefix<NT>(run, s.tot);
+    const int c = claim<NT>(run > 0.0 && goal < end, run > 0.0, s.mask);
+    int found = -1;
+    if (tid == c) {
+      double at = end - run;
+      for (int v = a0; v < a1; ++v) {
+        const double x = weight(value(p, v), q ? value(q, v) : 0.f);
+        if (x > 0.0) {
+          found = v;
+          at += x;
+          if (at > goal) break;
+        }
+      }
+    }
+    return found;                              // thread c's alone
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(kSplitT) void k_vp_sums(
+    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
+    const int32_t* __restrict__ draft_len, const float* __restrict__ uniforms, int L, int V,
+    int parts, int span, bool vec, double* __restrict__ sums, int32_t* __restrict__ accept_len) {
+  const int groups = parts / (kSplitT / kWave);
+  const int b = blockIdx.x / groups;
+  const int part = (blockIdx.x - b * groups) * (kSplitT / kWave) + threadIdx.x / kWave;
+  const Block<T> blk(target, draft, tokens, draft_len, uniforms, b, L, V);
+  const int n = blk.accepted();
+  const double s = part_sum(blk.p(n), blk.q(n), min(part * span, V), min((part + 1) * span, V), vec);
+  if (lane_id() == 0) {
+    sums[int64_t(b) * parts + part] = s;
     if (part == 0) accept_len[b] = n;
   }
 }
 
-template <typename T>
-__global__ __launch_bounds__(kT) void k_vp_draw(const T* __restrict__ target,
-                                                const T* __restrict__ draft,
-                                                const int32_t* __restrict__ draft_len,
-                                                const float* __restrict__ uniforms, int L, int V,
-                                                int span, int parts,
-                                                const Sums* __restrict__ sums,
-                                                const int32_t* __restrict__ accept_len,
-                                                int32_t* __restrict__ next_token) {
-  __shared__ Sums ps[kMaxParts];
-  __shared__ double wtot[kWavesV];
-  __shared__ double sbase, sgoal;
-  __shared__ int spart, ssecond;
-  __shared__ unsigned long long first_m[kWavesV], pos_m[kWavesV];
-  const int b = blockIdx.x, tid = threadIdx.x;
-  const int len = block_len(draft_len, b, L);
+template <class T>
+__global__ __launch_bounds__(kDrawT) void k_vp_draw(
+    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
+    const int32_t* __restrict__ draft_len, const float* __restrict__ uniforms, int L, int V,
+    int parts, int span, bool vec, const double* __restrict__ sums,
+    const int32_t* __restrict__ accept_len, int32_t* __restrict__ next_token) {
+  __shared__ DrawLds<kDrawT> s;
+  const int b = blockIdx.x;
+  const Block<T> blk(target, draft, tokens, draft_len, uniforms, b, L, V);
   const int n = accept_len[b];
-  for (int i = tid; i < parts; i += kT) ps[i] = sums[int64_t(b) * parts + i];
+  if (int(threadIdx.x) < parts) s.sum[threadIdx.x] = sums[int64_t(b) * parts + threadIdx.x];
   __syncthreads();
-  if (tid == 0) {
-    double tw = 0.0, tp = 0.0;
-    for (int i = 0; i < parts; ++i) {
-      tw += ps[i].w;
-      tp += ps[i].p;
-    }
-    const bool residual = n < len && tw > 0.0;       // else p_n itself
-    const double total = residual ? tw : tp;
-    const double goal = double(uniforms[int64_t(b) * (L + 1) + L]) * total;
-    double run = 0.0, base = 0.0;
-    int at = -1;
-    for (int i = 0; i < parts; ++i) {
-      const double s = residual ? ps[i].w : ps[i].p;
-      if (s > 0.0) {
-        at = i;                                      // the last part with weight, failing a hit
-        base = run;
-        if (goal < run + s) break;
-      }
-      run += s;
-    }
-    spart = at;
-    ssecond = residual;
-    sbase = base;
-    sgoal = goal;
-  }
-  __syncthreads();
-  const int part = spart;
-  if (part < 0) {                                    // no token has probability
-    if (tid == 0) next_token[b] = -1;
-    return;
-  }
-  const bool residual = ssecond != 0;
-  const double goal = sgoal;
-  const T* p = target + (int64_t(b) * (L + 1) + n) * V;
-  const T* q = draft + (int64_t(b) * L + (residual ? n : 0)) * V;
-  const int v0 = part * span, v1 = min(v0 + span, V);
-  // thread t owns a run of `each` tokens, so thread order is token order
-  const int each = (v1 - v0 + kT - 1) / kT;
-  const int a0 = min(v0 + tid * each, v1), a1 = min(a0 + each, v1);
-  auto weight = [&](int v) {
-    const double pv = clean(value(p, v));
-    const double qv = residual ? clean(value(q, v)) : 0.0;
-    return pv > qv ? pv - qv : 0.0;
-  };
-  double own = 0.0;
-  for (int v = a0; v < a1; ++v) own += weight(v);
-  // exclusive prefix over threads
-  double incl = own;
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const double o = __shfl_up(incl, d);
-    if (lane_id() >= d) incl += o;
-  }
-  if (lane_id() == kWave - 1) wtot[tid / kWave] = incl;
-  __syncthreads();
-  double before = sbase;
-  for (int w = 0; w < tid / kWave; ++w) before += wtot[w];
-  const bool pos = own > 0.0;
-  const unsigned long long fm = __ballot(pos && goal < before + incl);
-  const unsigned long long pm = __ballot(pos);
-  if (lane_id() == 0) {
-    first_m[tid / kWave] = fm;
-    pos_m[tid / kWave] = pm;
-  }
-  __syncthreads();
-  int claim = -1;
-  for (int w = 0; w < kWavesV && claim < 0; ++w)
-    if (first_m[w]) claim = w * kWave + __ffsll((long long)first_m[w]) - 1;
-  for (int w = kWavesV - 1; w >= 0 && claim < 0; --w)      // rounding: the last with weight
-    if (pos_m[w]) claim = w * kWave + 63 - __clzll((long long)pos_m[w]);
-  if (tid == claim) {
-    double run = before + incl - own;
-    int last = -1;
-    for (int v = a0; v < a1; ++v) {
-      const double x = weight(v);
-      if (x > 0.0) {
-        last = v;
-        run += x;
-        if (run > goal) break;
-      }
-    }
-    next_token[b] = last;
-  }
+  const int t = draw<kDrawT>(blk.p(n), blk.q(n), V, parts, span, blk.u[L], vec, s);
+  const bool any = __syncthreads_or(t >= 0);
+  if (t >= 0 || (!any && threadIdx.x == 0)) next_token[b] = t;
 }
 
-template <typename T>
+// One workgroup per block: its waves' parts are the row's.
+template <class T>
+__global__ __launch_bounds__(kOneT) void k_vp_one(
+    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
+    const int32_t* __restrict__ draft_len, const float* __restrict__ uniforms, int L, int V,
+    int span, bool vec, int32_t* __restrict__ accept_len, int32_t* __restrict__ next_token) {
+  constexpr int kParts = kOneT / kWave;
+  __shared__ DrawLds<kOneT> s;
+  const int b = blockIdx.x, part = threadIdx.x / kWave;
+  const Block<T> blk(target, draft, tokens, draft_len, uniforms, b, L, V);
+  const int n = blk.accepted();
+  const double sum =
+      part_sum(blk.p(n), blk.q(n), min(part * span, V), min((part + 1) * span, V), vec);
+  if (lane_id() == 0) s.sum[part] = sum;
+  __syncthreads();
+  const int t = draw<kOneT>(blk.p(n), blk.q(n), V, kParts, span, blk.u[L], vec, s);
+  const bool any = __syncthreads_or(t >= 0);
+  if (t >= 0 || (!any && threadIdx.x == 0)) next_token[b] = t;
+  if (threadIdx.x == 0) accept_len[b] = n;
+}
+
+template <class T>
 hipError_t launch_typed(const void* target, const void* draft, const int32_t* tokens,
                         const int32_t* draft_len, const float* uniforms, int B, int L, int V,
                         int32_t* accept_len, int32_t* next_token, void* workspace, hipStream_t s) {
-  const int parts = parts_of(B, V);
-  const int span = (V + parts - 1) / parts;
-  Sums* sums = static_cast<Sums*>(workspace);
   const T* p = static_cast<const T*>(target);
   const T* q = static_cast<const T*>(draft);
-  k_vp_sums<T><<<unsigned(B) * unsigned(parts), kT, 0, s>>>(p, q, tokens, draft_len, uniforms, L, V,
-                                                            span, parts, sums, accept_len);
-  k_vp_draw<T><<<unsigned(B), kT, 0, s>>>(p, q, draft_len, uniforms, L, V, span, parts, sums,
-                                          accept_len, next_token);
+  const bool vec = V % (16 / int(sizeof(T))) == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 &&
+                   reinterpret_cast<uintptr_t>(q) % 16 == 0;
+  if (one_launch(B, V)) {
+    k_vp_one<T><<<unsigned(B), kOneT, 0, s>>>(p, q, tokens, draft_len, uniforms, L, V,
+                                              span_of(V, kOneT / kWave), vec, accept_len, next_token);
+    return hipGetLastError();
+  }
+  const int parts = parts_of(B, V), span = span_of(V, parts);
+  double* sums = static_cast<double*>(workspace);
+  const unsigned groups = unsigned(parts / (kSplitT / kWave));
+  k_vp_sums<T><<<unsigned(B) * groups, kSplitT, 0, s>>>(p, q, tokens, draft_len, uniforms, L, V,
+                                                        parts, span, vec, sums, accept_len);
+  k_vp_draw<T><<<unsigned(B), kDrawT, 0, s>>>(p, q, tokens, draft_len, uniforms, L, V, parts, span,
+                                              vec, sums, accept_len, next_token);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// one pair of sums per block and part
+// the parts' sums, where two launches are taken
 size_t verify_probs_workspace_bytes(int B, int V) {
-  return size_t(B) * parts_of(B, V) * sizeof(Sums);
+  return one_launch(B, V) ? 0 : size_t(B) * parts_of(B, V) * sizeof(double);
 }
 
 hipError_t launch_verify_probs(const void* target, const void* draft, bool bf16,

@@ -344,17 +344,36 @@ def moe_mxfp4_layer_noalloc(x, logits, k, w13_codes, w13_scales, w2_codes, w2_sc
 
 def _enqueue(name, device, *args):
     """Call the library on `device`'s current stream (whatever device is current)."""
-    if device.index == torch.cuda.current_device():
-        check(getattr(lib(), name)(*args, _stream()), name)
+    i = device.index
+    if i == torch._C._cuda_getDevice():
+        st = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
         with torch.cuda.device(device):
-            check(getattr(lib(), name)(*args, _stream()), name)
+            st = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(i))
+    if st:
+        check(st, name)
+
+
+def _want(t, name, dtype, shape, device):
+    """_need, quickly where it holds: a call makes five of these checks and
+    lasts a few microseconds itself."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and
+            t.get_device() == device.index and t.is_contiguous()):
+        _need(t, name, dtype, shape, device)
+
+
+def _result(t, name, dtype, shape, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _want(t, name, dtype, shape, device)
+    return t
 
 
 def _need_mx(codes, scales, name, shape, device):
     """codes uint8 [*shape[:-1], K/2] and scales uint8 [*shape[:-1], K/32] of an MXFP4 tensor."""
-    _need(codes, name + "_codes", torch.uint8, (*shape[:-1], shape[-1] // 2), device)
-    _need(scales, name + "_scales", torch.uint8, (*shape[:-1], shape[-1] // 32), device)
+    rows, K = shape[:-1], shape[-1]
+    _want(codes, name + "_codes", torch.uint8, rows + (K // 2,), device)
+    _want(scales, name + "_scales", torch.uint8, rows + (K // 32,), device)
 
 
 def _rank(t, name, n):
@@ -373,7 +392,7 @@ def mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, dtype=torch.float32, out=No
     K, dev = 2 * half, a_codes.device
     _need_mx(a_codes, a_scales, "a", (M, K), dev)
     _need_mx(b_codes, b_scales, "b", (N, K), dev)
-    out = _out(out, "out", dtype, (M, N), dev)
+    out = _result(out, "out", dtype, (M, N), dev)
     _enqueue("mxfp4_gemm", dev, _ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), M, N,
              K, _ptr(out), BF16 if dtype == torch.bfloat16 else F32)
     return out
@@ -385,8 +404,8 @@ def _a4_gate_up_shapes(x_codes, x_scales, sorted_pairs, offsets, k, w13_codes, w
     H, I, dev = 2 * half, two_i // 2, x_codes.device
     _need_mx(x_codes, x_scales, "x", (T, H), dev)
     _need_mx(w13_codes, w13_scales, "w13", (E, 2 * I, H), dev)
-    _need(sorted_pairs, "sorted_pairs", torch.int32, (T * k,), dev)
-    _need(offsets, "offsets", torch.int32, (E + 1,), dev)
+    _want(sorted_pairs, "sorted_pairs", torch.int32, (T * k,), dev)
+    _want(offsets, "offsets", torch.int32, (E + 1,), dev)
     return T, H, I, E, dev
 
 
@@ -395,7 +414,7 @@ def moe_mxfp4_a4_gate_up_swiglu(x_codes, x_scales, sorted_pairs, offsets, k, w13
     """MXFP4 x [T, H] -> h [T*k, I] bfloat16 (rows in sorted order)."""
     T, H, I, E, dev = _a4_gate_up_shapes(x_codes, x_scales, sorted_pairs, offsets, k, w13_codes,
                                          w13_scales)
-    h = _out(h, "h", torch.bfloat16, (T * k, I), dev)
+    h = _result(h, "h", torch.bfloat16, (T * k, I), dev)
     _enqueue("moe_mxfp4_a4_gate_up_swiglu", dev, _ptr(x_codes), _ptr(x_scales), _ptr(sorted_pairs),
              _ptr(offsets), T, H, I, E, k, _ptr(w13_codes), _ptr(w13_scales), _ptr(h), None, None)
     return h
@@ -407,8 +426,8 @@ def moe_mxfp4_a4_gate_up_swiglu_pack(x_codes, x_scales, sorted_pairs, offsets, k
     bfloat16 h, bit for bit) -> (h_codes [T*k, I/2], h_scales [T*k, I/32])."""
     T, H, I, E, dev = _a4_gate_up_shapes(x_codes, x_scales, sorted_pairs, offsets, k, w13_codes,
                                          w13_scales)
-    h_codes = _out(h_codes, "h_codes", torch.uint8, (T * k, I // 2), dev)
-    h_scales = _out(h_scales, "h_scales", torch.uint8, (T * k, I // 32), dev)
+    h_codes = _result(h_codes, "h_codes", torch.uint8, (T * k, I // 2), dev)
+    h_scales = _result(h_scales, "h_scales", torch.uint8, (T * k, I // 32), dev)
     _enqueue("moe_mxfp4_a4_gate_up_swiglu", dev, _ptr(x_codes), _ptr(x_scales), _ptr(sorted_pairs),
              _ptr(offsets), T, H, I, E, k, _ptr(w13_codes), _ptr(w13_scales), None, _ptr(h_codes),
              _ptr(h_scales))
@@ -424,8 +443,8 @@ def moe_mxfp4_a4_down(h_codes, h_scales, offsets, k, w2_codes, w2_scales, y=None
         raise ValueError("h must have T*k rows")
     _need_mx(h_codes, h_scales, "h", (R, I), dev)
     _need_mx(w2_codes, w2_scales, "w2", (E, H, I), dev)
-    _need(offsets, "offsets", torch.int32, (E + 1,), dev)
-    y = _out(y, "y", torch.float32, (R, H), dev)
+    _want(offsets, "offsets", torch.int32, (E + 1,), dev)
+    y = _result(y, "y", torch.float32, (R, H), dev)
     _enqueue("moe_mxfp4_a4_down", dev, _ptr(h_codes), _ptr(h_scales), _ptr(offsets), R // k, H, I,
              E, k, _ptr(w2_codes), _ptr(w2_scales), _ptr(y))
     return y
@@ -462,8 +481,8 @@ def moe_mxfp4_a4_layer(x, logits, k, w13_codes, w13_scales, w2_codes, w2_scales,
     T, H = _rank(x, "x", 2)
     E, two_i, _ = _rank(w13_codes, "w13_codes", 3)
     I, dev = two_i // 2, x.device
-    _need(x, "x", torch.bfloat16)
-    _need(logits, "logits", torch.float32, (T, E), dev)
+    _want(x, "x", torch.bfloat16, (T, H), dev)
+    _want(logits, "logits", torch.float32, (T, E), dev)
     _need_mx(w13_codes, w13_scales, "w13", (E, 2 * I, H), dev)
     _need_mx(w2_codes, w2_scales, "w2", (E, H, I), dev)
     b = buffers if buffers is not None else A4LayerBuffers(T, H, I, E, k, dev)
@@ -491,22 +510,23 @@ def dflash_verify_probs(target_probs, draft_probs, draft_tokens, uniforms, draft
     dev, dtype = draft_probs.device, draft_probs.dtype
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("draft_probs must be float32 or bfloat16")
-    _need(draft_probs, "draft_probs", dtype)
-    _need(target_probs, "target_probs", dtype, (B, L + 1, V), dev)
-    _need(draft_tokens, "draft_tokens", torch.int32, (B, L), dev)
-    _need(uniforms, "uniforms", torch.float32, (B, L + 1), dev)
+    _want(draft_probs, "draft_probs", dtype, (B, L, V), dev)
+    _want(target_probs, "target_probs", dtype, (B, L + 1, V), dev)
+    _want(draft_tokens, "draft_tokens", torch.int32, (B, L), dev)
+    _want(uniforms, "uniforms", torch.float32, (B, L + 1), dev)
     if draft_len is not None:
-        _need(draft_len, "draft_len", torch.int32, (B,), dev)
-    accept_len = _out(accept_len, "accept_len", torch.int32, (B,), dev)
-    next_token = _out(next_token, "next_token", torch.int32, (B,), dev)
+        _want(draft_len, "draft_len", torch.int32, (B,), dev)
+    accept_len = _result(accept_len, "accept_len", torch.int32, (B,), dev)
+    next_token = _result(next_token, "next_token", torch.int32, (B,), dev)
     if workspace is None:
-        workspace = torch.empty(max(dflash_verify_probs_workspace_bytes(B, L, V), 8),
-                                dtype=torch.uint8, device=dev)
-    _need(workspace, "workspace", torch.uint8, None, dev)
+        need = dflash_verify_probs_workspace_bytes(B, L, V)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        _need(workspace, "workspace", torch.uint8, None, dev)
     _enqueue("dflash_verify_probs", dev, _ptr(target_probs), _ptr(draft_probs),
              BF16 if dtype == torch.bfloat16 else F32, _ptr(draft_tokens), _ptr(draft_len),
              _ptr(uniforms), B, L, V, _ptr(accept_len), _ptr(next_token), _ptr(workspace),
-             workspace.numel())
+             0 if workspace is None else workspace.numel())
     return accept_len, next_token
 
 

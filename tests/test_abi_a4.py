@@ -83,23 +83,25 @@ def test_layer_argument_checks(lib):
 def test_verify_probs_argument_checks(lib):
     f = lib.dflash_verify_probs
     # p, q, dtype, tokens, len, u, B, L, V, accept, next, ws, bytes, stream
-    ws = lib.dflash_verify_probs_workspace_bytes(4, 8, 50)
+    V = 50000
+    ws = lib.dflash_verify_probs_workspace_bytes(4, 8, V)
     assert ws > 0
+    assert lib.dflash_verify_probs_workspace_bytes(4, 8, 50) == 0      # one launch: none needed
     assert lib.dflash_verify_probs_workspace_bytes(4, 33, 50) == 0
     assert lib.dflash_verify_probs_workspace_bytes(4, 8, 0) == 0
     assert lib.dflash_verify_probs_workspace_bytes(0, 8, 50) == 0
-    assert f(P, P, 5, P, None, P, 4, 8, 50, P, P, P, ws, None) == -3
-    assert f(P, P, 0, P, None, P, 4, 0, 50, P, P, P, ws, None) == -2
-    assert f(P, P, 0, P, None, P, 4, 33, 50, P, P, P, ws, None) == -2
+    assert f(P, P, 5, P, None, P, 4, 8, V, P, P, P, ws, None) == -3
+    assert f(P, P, 0, P, None, P, 4, 0, V, P, P, P, ws, None) == -2
+    assert f(P, P, 0, P, None, P, 4, 33, V, P, P, P, ws, None) == -2
     assert f(P, P, 0, P, None, P, 4, 8, 0, P, P, P, ws, None) == -2
-    assert f(P, P, 0, P, None, P, (1 << 24) + 1, 8, 50, P, P, P, 1 << 40, None) == -2
-    assert f(P, P, 0, P, None, P, 4, 8, 50, P, P, P, ws - 1, None) == -7
-    assert f(P, None, 0, P, None, P, 4, 8, 50, P, P, P, ws, None) == -1
-    assert f(P, P, 0, P, None, P, 4, 8, 50, P, P, None, ws, None) == -1
-    assert f(P + 2, P, 0, P, None, P, 4, 8, 50, P, P, P, ws, None) == -4
-    assert f(P, P + 1, 1, P, None, P, 4, 8, 50, P, P, P, ws, None) == -4
-    assert f(P, P, 1, P, P + 2, P, 4, 8, 50, P, P, P, ws, None) == -4
-    assert f(P, P, 1, P, None, P, 4, 8, 50, P, P, P + 4, ws, None) == -4
+    assert f(P, P, 0, P, None, P, (1 << 24) + 1, 8, V, P, P, P, 1 << 40, None) == -2
+    assert f(P, P, 0, P, None, P, 4, 8, V, P, P, P, ws - 1, None) == -7
+    assert f(P, None, 0, P, None, P, 4, 8, V, P, P, P, ws, None) == -1
+    assert f(P, P, 0, P, None, P, 4, 8, V, P, P, None, ws, None) == -1
+    assert f(P + 2, P, 0, P, None, P, 4, 8, V, P, P, P, ws, None) == -4
+    assert f(P, P + 1, 1, P, None, P, 4, 8, V, P, P, P, ws, None) == -4
+    assert f(P, P, 1, P, P + 2, P, 4, 8, V, P, P, P, ws, None) == -4
+    assert f(P, P, 1, P, None, P, 4, 8, V, P, P, P + 4, ws, None) == -4
     assert f(None, None, 0, None, None, None, 0, 8, 50, None, None, None, 0, None) == 0
 
 
