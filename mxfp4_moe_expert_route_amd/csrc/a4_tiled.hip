@@ -56,11 +56,12 @@ struct Lds {
   static constexpr int kRingW = AS == 4 ? (MS == 1 ? 4 : 3) : 5;
   static constexpr int kXLoads = (kXSlot / 1024 + kWaves - 1) / kWaves;
   static constexpr int kWLoads = kWSlot / 1024 / kWaves;     // per wave and stage
+  static constexpr int kSRows = kNT + kMT;                   // rows of scales, 32 bytes each
+  static constexpr int kSLoads = (kSRows / 32 + kWaves - 1) / kWaves;
   static constexpr int kMTw = (kMT + kWave - 1) / kWave * kWave;   // whole waves of rows
-  static constexpr int kSRows = kNT + kMTw;
   static constexpr int kX = kRingW * kWSlot;
   static constexpr int kS = kX + kRingX * kXSlot;
-  static constexpr int kTok = kS + 2 * kSRows * 16;
+  static constexpr int kTok = kS + kSRows * 32;
   static constexpr int kItems = kTok + 2 * kMTw * 4;
   static constexpr int kBytes = kItems + kBatch * 16;
   static_assert(kBytes <= 160 * 1024, "LDS per CU");
@@ -113,9 +114,29 @@ struct Item {
   int e, n, row0, rows;
 };
 
-// The scale bytes of block g of a stage's two steps, in bytes 0 and 1.
-__device__ __forceinline__ uint32_t pick(u32x2 v, uint32_t sel) {
-  return __builtin_amdgcn_perm(v.y, v.x, sel);
+// The lane id, as a value of its own: what the rarely run parts derive from it
+// is computed there and holds no register in between.
+__device__ __forceinline__ int lane_here() {
+  int l = lane_id();
+  asm volatile("" : "+v"(l));
+  return l;
+}
+
+// 32-bit product in one register (a multiply-add would hold two)
+__device__ __forceinline__ uint32_t times(int a, int b) {
+  uint32_t v = uint32_t(a) * uint32_t(b);
+  asm("" : "+v"(v));
+  return v;
+}
+
+// The 4 x 4 bytes of four dwords transposed: dword g gets their bytes g.
+__device__ __forceinline__ u32x4 transpose4(u32x4 v) {
+  const uint32_t a = __builtin_amdgcn_perm(v.y, v.x, 0x05010400u);   // x0 y0 x1 y1
+  const uint32_t b = __builtin_amdgcn_perm(v.y, v.x, 0x07030602u);   // x2 y2 x3 y3
+  const uint32_t c = __builtin_amdgcn_perm(v.w, v.z, 0x05010400u);
+  const uint32_t d = __builtin_amdgcn_perm(v.w, v.z, 0x07030602u);
+  return u32x4{__builtin_amdgcn_perm(c, a, 0x05040100u), __builtin_amdgcn_perm(c, a, 0x07060302u),
+               __builtin_amdgcn_perm(d, b, 0x05040100u), __builtin_amdgcn_perm(d, b, 0x07060302u)};
 }
 
 // acc += W X for byte B of the packed scales
@@ -127,8 +148,8 @@ __device__ __forceinline__ f32x4 mfma_step(u32x4 w, uint32_t sw, u32x4 x, uint32
                                                           int(sx));
 }
 
-// KIND, OUT as in a4.hpp; AS: weight subtiles per wave; WHOLE: K is a
-// multiple of 512 and scale rows are 16-byte aligned.
+// KIND, OUT as in a4.hpp; AS, MS: weight and row subtiles per wave; WHOLE: K
+// is a multiple of 512 and scale rows are 16-byte aligned.
 template <Kind KIND, Out OUT, int AS, int MS, bool WHOLE>
 struct Tiled {
   using L = Lds<AS, MS>;
@@ -139,28 +160,32 @@ struct Tiled {
   const Problem& p;
   uint8_t* lds;
   int wave, lane, r16, g, wn, wm;
-  int nst, nblk, rowb;
+  int nst, nblk, rowb;              // stages per item (an even number), blocks and bytes per row
   int cnt;                          // items of the batch
 
-  // loaders: activations and scales (two stages ahead), weights (kRingW ahead)
+  // the activation (and scale) stream, two stages ahead
   int xi = 0, xs = 0, xt = 0;       // item, stage in it, stage overall
-  int xchunk = 0;                   // scale chunks issued
-  int nx = 0;                       // activation loads of this wave per stage
+  int xdst = 0, xso = 0;            // LDS slot and offset in the rows of the stage at hand
+  uint32_t xtail = 0;
   uint32_t xoff[L::kXLoads];
-  const uint8_t* sptr = nullptr;    // this lane's scale row
-  bool srow = false;                // the wave loads scales for this item
+  uint32_t soff[L::kSLoads];        // this lane's scale rows
+  const uint8_t* swbase = nullptr;
+  u32x4 spend[L::kSLoads];          // scales on their way from memory to LDS
+  bool sfull = false;
+  // the weight stream, kRingW stages ahead
   int wi = 0, wst = 0, wt = 0;
-  uint32_t woff[L::kWLoads];
+  int wdst = 0, wso = 0, wbytes = 0;
+  uint32_t wlane;                   // this lane's piece of a load's first row
   const uint8_t* wbase = nullptr;
-  int young = 0;                    // loads and stores issued since the last one waited for
-  // without WHOLE: scale bytes on their way from memory to LDS
-  uint32_t spend[4];
-  int spend_slot = -1;
+  int stores = 0;                   // of the epilogue before
+  // where this lane's pieces of step kk and its scales lie in a subtile
+  int wat[2], xat[2], swat, sxat;
 
   // compute: weights of the step at hand (each subtile is replaced by the next
-  // step's once it is used), activations of a stage's two steps, scales
+  // step's once it is used), activations of a stage's two steps, the scales of
+  // a pair of stages (a byte per step)
   u32x4 w[AS], xa[MS], xb[MS];
-  uint32_t sw[AS], sx[MS], sxn[MS];
+  uint32_t sw[AS], sx[MS];
   f32x4 acc[AS][MS];
 
   __device__ __forceinline__ Tiled(const Problem& q, uint8_t* l) : p(q), lds(l) {
@@ -171,8 +196,17 @@ struct Tiled {
     wn = wave % kWN;
     wm = wave / kWN;
     nblk = p.K / 32;
-    nst = (nblk + 7) / 8;
+    nst = 2 * ((nblk + 15) / 16);
     rowb = p.K / 2;
+    wlane = uint32_t(8 * wave + (lane >> 3)) * uint32_t(rowb) + 16u * ((lane & 7) ^ (lane >> 3));
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const int at = 16 * ((4 * kk + g) ^ (r16 & 7)) + 128 * r16;
+      wat[kk] = at + 128 * sub_row(0);
+      xat[kk] = at + 128 * 16 * wm + L::kX;
+    }
+    swat = L::kS + 32 * (sub_row(0) + r16) + 16 * (r16 >> 3) + 4 * g;
+    sxat = L::kS + 32 * (L::kNT + 16 * wm + r16) + 16 * (r16 >> 3) + 4 * g;
   }
 
   __device__ __forceinline__ Item item(int i) const {
@@ -197,16 +231,17 @@ struct Tiled {
   }
 
   // Row of X of tile row j (< rows) of the item whose tokens are in slot `par`.
-  __device__ __forceinline__ int64_t xrow(const Item& it, int par, int j) const {
+  __device__ __forceinline__ int xrow(const Item& it, int par, int j) const {
     if constexpr (kGU) return lds_read_i32(lds + L::kTok + par * L::kMTw * 4 + 4 * j) / p.k;
-    else return int64_t(it.row0) + j;
+    else return it.row0 + j;
   }
 
-  // pair ids of an item's rows -> token slot (waves 0 .. 2, one load each)
+  // pair ids of an item's rows -> token slot, one load per 64 rows
   __device__ __forceinline__ void issue_tokens(int i) {
     if constexpr (kGU) {
       if (wave < L::kMTw / kWave && i < cnt) {
         const Item it = item(i);
+        const int lane = lane_here();
         const int32_t* src = p.pairs + it.row0 + min(wave * kWave + lane, it.rows - 1);
         __builtin_amdgcn_global_load_lds(
             src, lds_at(lds, L::kTok + (i & 1) * L::kMTw * 4 + wave * kWave * 4), 4, 0, 0);
@@ -214,115 +249,133 @@ struct Tiled {
     }
   }
 
+  // Scale load h of this wave: 32 rows, two lanes each; weight rows first.
+  // A lane's 16 bytes are the blocks 4 j + g of four steps j of 128; they go to
+  // LDS transposed, so that lane group g finds its bytes of the four steps in
+  // one dword.  Row r keeps its half b at slot b ^ (r / 8 % 2): the 16 rows of
+  // a subtile are read without bank conflicts.
+  __device__ __forceinline__ int sload(int h) const { return wave + kWaves * h; }
+  __device__ __forceinline__ bool sload_w(int h) const { return sload(h) < L::kNT / 32; }
+  __device__ __forceinline__ bool sload_any(int h) const { return sload(h) < L::kSRows / 32; }
+
   __device__ __forceinline__ void x_item() {
     const Item it = item(xi);
+    const int lane = lane_here();
     const int rl = lane >> 3;
-    nx = 0;
 #pragma unroll
     for (int q = 0; q < L::kXLoads; ++q) {
-      const int j0 = 8 * (wave + kWaves * q);
-      if (j0 < it.rows) ++nx;
-      const int j = min(j0 + rl, it.rows - 1);
-      xoff[q] = uint32_t(xrow(it, xi & 1, j)) * uint32_t(rowb) + 16u * ((lane & 7) ^ rl) +
-                (j0 + rl >= it.rows ? kDead : 0u);
+      const int j = 8 * (wave + kWaves * q) + rl;
+      xoff[q] = times(xrow(it, xi & 1, min(j, it.rows - 1)), rowb) + 16u * ((lane & 7) ^ rl) +
+                (j >= it.rows ? kDead : 0u);
     }
-    const int sr = (wave & 3) * kWave + lane;
-    if (wave < kWN) {
-      srow = sr < L::kNT;
-      sptr = p.ws + (erow(it.e) + wrow(it.n, sr)) * nblk;
-    } else {
-      srow = (wave & 3) * kWave < it.rows;
-      sptr = p.xs + xrow(it, xi & 1, min(sr, it.rows - 1)) * nblk;
+    swbase = p.ws + erow(it.e) * nblk;
+#pragma unroll
+    for (int h = 0; h < L::kSLoads; ++h) {
+      const int r = 32 * sload(h) + (lane >> 1);
+      soff[h] = times(sload_w(h) ? wrow(it.n, r)
+                                 : xrow(it, xi & 1, max(0, min(r - L::kNT, it.rows - 1))), nblk);
     }
   }
 
-  __device__ __forceinline__ int sslot(int chunk) const { return L::kS + (chunk & 1) * L::kSRows * 16; }
-  __device__ __forceinline__ int srow_off() const {
-    return ((wave < kWN ? 0 : L::kNT) + (wave & 3) * kWave) * 16;
-  }
-
-  // activations (and, for a new pair of stages, scales) of the next stage of
-  // the activation stream
-  __device__ __forceinline__ void issue_x(const __amdgpu_buffer_rsrc_t& rx) {
-    if (xi >= cnt) return;
-    if (xs == 0) x_item();
-    if ((xs & 1) == 0) {
-      if (srow) {
-        if constexpr (WHOLE) {
-          __builtin_amdgcn_global_load_lds(sptr + 8 * xs, lds_at(lds, sslot(xchunk) + srow_off()), 16,
-                                           0, 0);
-        } else {
+  // Scales of stages 4 c .. 4 c + 3 of the activation stream's item, at its
+  // stage 4 c: into registers here, to LDS before the next barrier.  One
+  // buffer does: a pair of stages' scales are read in the stage before it, so
+  // past this point the last of the four before are in registers, and the
+  // first of these are read behind the next barrier.
+  __device__ __forceinline__ void load_scales() {
+    const int lane = lane_here();
+    const int half = (lane & 1) ^ ((lane >> 4) & 1);
 #pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            uint32_t v = 0;
+    for (int h = 0; h < L::kSLoads; ++h) {
+      if (!sload_any(h)) continue;
+      const int b0 = 8 * xs + 16 * half;                // first block of this lane's half
+      const uint8_t* src = (sload_w(h) ? swbase : p.xs) + soff[h];
+      if constexpr (WHOLE) {
+        // a half past the row's end is not used; it reads the row's first
+        spend[h] = *reinterpret_cast<const u32x4*>(src + (b0 < nblk ? b0 : 0));
+      } else {
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const int blk = 8 * xs + 4 * d + b;
-              v |= (blk < nblk ? uint32_t(sptr[blk]) : 127u) << (8 * b);
-            }
-            spend[d] = v;
+        for (int d = 0; d < 4; ++d) {
+          uint32_t v = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int blk = b0 + 4 * d + b;
+            v |= (blk < nblk ? uint32_t(src[blk]) : 127u) << (8 * b);
           }
-          spend_slot = sslot(xchunk);
+          spend[h][d] = v;
         }
       }
-      ++xchunk;
     }
-    const uint32_t tail =
-        !WHOLE && 8 * xs + int((lane & 7) ^ (lane >> 3)) >= nblk ? kDead : 0u;
+    sfull = true;
+  }
+  __device__ __forceinline__ void flush_scales() {
+    if (sfull) {
 #pragma unroll
-    for (int q = 0; q < L::kXLoads; ++q)
-      if (q < nx)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rx, lds_at(lds, L::kX + (xt & 1) * L::kXSlot + 1024 * (wave + kWaves * q)), 16,
-            (xoff[q] + 128u * xs) | tail, 0, 0, 0);
+      for (int h = 0; h < L::kSLoads; ++h)
+        if (sload_any(h))
+          *reinterpret_cast<u32x4*>(lds + L::kS + 1024 * sload(h) + 16 * lane) = transpose4(spend[h]);
+    }
+    sfull = false;
+  }
+
+  // Next stage of the activation stream: where it goes; a new item's rows; new
+  // scales.  Past the stream's end the loads are dead: they move nothing, and
+  // keep the count of loads the same in every stage.
+  __device__ __forceinline__ void next_x() {
+    xdst = L::kX + (xt & 1) * L::kXSlot;
+    xso = 128 * xs;
+    xtail = 0;
     ++xt;
+    if (xi >= cnt) {
+      xtail = kDead;
+      return;
+    }
+    if (xs == 0) x_item();
+    if ((xs & 3) == 0) load_scales();
+    if (!WHOLE && 8 * xs + int((lane & 7) ^ (lane >> 3)) >= nblk) xtail = kDead;
     if (++xs == nst) {
       xs = 0;
       ++xi;
     }
   }
-
-  // scale bytes that came through registers go to LDS before the barrier
-  // after which they are read
-  __device__ __forceinline__ void flush_scales() {
-    if constexpr (!WHOLE) {
-      if (spend_slot >= 0)
-        *reinterpret_cast<u32x4*>(lds + spend_slot + srow_off() + 16 * lane) =
-            u32x4{spend[0], spend[1], spend[2], spend[3]};
-      spend_slot = -1;
-    }
+  __device__ __forceinline__ void load_x(const __amdgpu_buffer_rsrc_t& rx, int q) {
+    if (L::kXSlot / 1024 % kWaves && wave + kWaves * q >= L::kXSlot / 1024) return;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, lds_at(lds, xdst + 1024 * (wave + kWaves * q)), 16,
+                                             xoff[q] | xtail, xso, 0, 0);
   }
 
+  // A tile's weight rows are those of the expert from its first on (gate/up:
+  // and N further on, the up rows).  Rows past the last column are other
+  // rows, or zeros past the expert's end; so are pieces past a row's end, which
+  // meet zero activations.  None of their sums is stored.
   __device__ __forceinline__ void w_item() {
     const Item it = item(wi);
-    const int rl = lane >> 3;
-    const int r0 = kGU ? 0 : it.n * kCols;               // the first row the base stands for
-    wbase = p.wc + (erow(it.e) + r0) * rowb;
-#pragma unroll
-    for (int q = 0; q < L::kWLoads; ++q)
-      woff[q] = uint32_t(wrow(it.n, 8 * (wave + kWaves * q) + rl) - r0) * uint32_t(rowb) +
-                16u * ((lane & 7) ^ rl);
+    const int64_t rows = int64_t(kGU ? 2 : 1) * p.N - it.n * kCols;
+    wbase = p.wc + (erow(it.e) + it.n * kCols) * rowb;
+    wbytes = int(rows * rowb < 0x7fffffff ? rows * rowb : 0x7fffffff);
   }
-
-  __device__ __forceinline__ int issue_w() {
-    if (wi >= cnt) return 0;
-    if (wst == 0) w_item();
-    const __amdgpu_buffer_rsrc_t rw =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(wbase), 0, 0x7fffffff, 0x00020000);
-    // a piece past the row's end meets zero activations; it reads the row's first
-    const bool past = !WHOLE && 8 * wst + int((lane & 7) ^ (lane >> 3)) >= nblk;
-    const uint32_t back = past ? 128u * wst + 16u * ((lane & 7) ^ (lane >> 3)) : 0u;
-    const int slot = (wt % L::kRingW) * L::kWSlot;
-#pragma unroll
-    for (int q = 0; q < L::kWLoads; ++q)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, lds_at(lds, slot + 1024 * (wave + kWaves * q)), 16,
-                                               woff[q] + 128u * wst - back, 0, 0, kAux);
+  __device__ __forceinline__ void next_w() {
+    wdst = (wt % L::kRingW) * L::kWSlot;
+    wso = 128 * wst;
     ++wt;
+    if (wi >= cnt) {
+      wbytes = 0;                            // dead loads: out of range
+      return;
+    }
+    if (wst == 0) w_item();
     if (++wst == nst) {
       wst = 0;
       ++wi;
     }
-    return L::kWLoads;
+  }
+  __device__ __forceinline__ void load_w(int q) {
+    const __amdgpu_buffer_rsrc_t rw =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(wbase), 0, wbytes, 0x00020000);
+    const int lr0 = 8 * kWaves * q;          // first local row of the load
+    const int row0 = kGU && lr0 >= kCols ? p.N + lr0 - kCols : lr0;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, lds_at(lds, wdst + 1024 * (wave + kWaves * q)), 16,
+                                             wlane + uint32_t(row0) * uint32_t(rowb) + uint32_t(wso), 0,
+                                             0, kAux);
   }
 
   // this wave's weight subtile a as a local weight row
@@ -330,35 +383,26 @@ struct Tiled {
     if constexpr (kGU) return (a < AS / 2 ? 0 : kCols) + 16 * (AS / 2) * wn + 16 * (a % (AS / 2));
     else return 16 * AS * wn + 16 * a;
   }
-
-  // where this lane's pieces of step kk lie, from the start of a 16-row subtile
-  __device__ __forceinline__ int piece(int kk) const {
-    return 16 * ((4 * kk + g) ^ (r16 & 7)) + 128 * r16;
-  }
-  // weight subtile a of step kk of stage t
+  // weight subtile a of step kk of stage t; a's distance from subtile 0 is a
+  // constant, so it goes into the read's offset
   __device__ __forceinline__ void read_w(int t, int kk, int a) {
-    w[a] = *reinterpret_cast<const u32x4*>(lds + (t % L::kRingW) * L::kWSlot + piece(kk) +
-                                           128 * sub_row(a));
+    w[a] = *reinterpret_cast<const u32x4*>(lds + ((t % L::kRingW) * L::kWSlot + wat[kk]) +
+                                           128 * (sub_row(a) - sub_row(0)));
   }
   __device__ __forceinline__ void read_x(int t, int kk, u32x4 (&x)[MS]) const {
-    const uint8_t* b = lds + L::kX + (t & 1) * L::kXSlot + 128 * 16 * wm + piece(kk);
+    const uint8_t* b = lds + ((t & 1) * L::kXSlot + xat[kk]);
 #pragma unroll
     for (int i = 0; i < MS; ++i) x[i] = *reinterpret_cast<const u32x4*>(b + 128 * 16 * kWM * i);
   }
-
-  // scales of stage s of an item whose first scale chunk is c
-  __device__ __forceinline__ const uint8_t* scales_at(int c, int s) const {
-    return lds + sslot(c + (s >> 1)) + 16 * r16 + 8 * (s & 1);
+  // this lane's scales of stages 2 pr and 2 pr + 1 of an item, a byte per step
+  __device__ __forceinline__ void read_sw(int pr, int a) {
+    sw[a] = *reinterpret_cast<const uint32_t*>(lds + (swat ^ (16 * (pr & 1))) +
+                                               32 * (sub_row(a) - sub_row(0)));
   }
-  __device__ __forceinline__ uint32_t scale_pair(const uint8_t* s) const {
-    return pick(*reinterpret_cast<const u32x2*>(s), 0x0c0c0400u + 0x0101u * g);   // bytes g
-  }
-  __device__ __forceinline__ void read_sw(const uint8_t* sc, int a) {
-    sw[a] = scale_pair(sc + 16 * sub_row(a));
-  }
-  __device__ __forceinline__ void read_sx(const uint8_t* sc, uint32_t (&x)[MS]) const {
+  __device__ __forceinline__ void read_sx(int pr) {
+    const uint8_t* b = lds + (sxat ^ (16 * (pr & 1)));
 #pragma unroll
-    for (int i = 0; i < MS; ++i) x[i] = scale_pair(sc + 16 * (L::kNT + 16 * (wm + kWM * i)));
+    for (int i = 0; i < MS; ++i) sx[i] = *reinterpret_cast<const uint32_t*>(b + 32 * 16 * kWM * i);
   }
 
   // a step's products; then(a) runs once weight subtile a is used
@@ -368,13 +412,27 @@ struct Tiled {
     for (int a = 0; a < AS; ++a) {
 #pragma unroll
       for (int i = 0; i < MS; ++i) acc[a][i] = mfma_step<B>(w[a], sw[a], x[i], sx[i], acc[a][i]);
+      // the products are made here, not wherever their sums are next used
+#pragma unroll
+      for (int i = 0; i < MS; ++i) asm volatile("" : "+v"(acc[a][i]));
       then(a);
+      __builtin_amdgcn_sched_barrier(0);       // keeps loads and reads where they stand
     }
+  }
+  // A step's share of n loads after subtile a: spread over the step, since a
+  // burst of all waves' loads stalls their products.
+  template <class F>
+  __device__ __forceinline__ void spread(int n, int a, F&& load) {
+    const int per = (n + AS - 1) / AS;
+#pragma unroll
+    for (int q = 0; q < n; ++q)
+      if (q / per == a) load(q);
   }
 
   __device__ __forceinline__ int epilogue(const Item& it) {
-    int stores = 0;
+    int n = 0;
     const int64_t row0 = it.row0;
+    const int lane = lane_here(), r16 = lane & 15, g = lane >> 4;
     if constexpr (OUT == kMx) {
       // a wave's two gate subtiles are one MX block: h rounded to bf16, then
       // packed; the block is this lane's eight and those of lanes +-16, +-32
@@ -422,7 +480,7 @@ struct Tiled {
             0, 0);
         __builtin_amdgcn_raw_buffer_store_b8(
             uint8_t(e), rs, live && g == 0 ? uint32_t(j) * (p.N / 32) + blk : kDead, 0, 0);
-        stores += 2;
+        n += 2;
       }
     } else {
       constexpr int kSize = OUT == kF32 ? 4 : 2;
@@ -472,65 +530,79 @@ struct Tiled {
                                                           live && col + c < p.N ? at + 2 * c : kDead, 0, 0);
             }
           }
-          stores += 1;                       // at least
+          n += 1;                            // at least
         }
       }
     }
-    return stores;
+    return n;
+  }
+
+  // Stage t of the stream, an item's first (FIRST), last (LAST) or another
+  // one; PAR: its parity.  The loads due behind its barrier are spread over
+  // the products: activations in its second step, weights in the next stage's
+  // first (in this one's second where an epilogue lies between).  At the
+  // barrier everything but the youngest weights (and the stores after them)
+  // has to have landed.
+  template <int PAR, bool FIRST, bool LAST>
+  __device__ __forceinline__ void stage(int t, int pr, int i, const __amdgpu_buffer_rsrc_t& rx) {
+    read_x(t, 1, xb);
+    step<2 * PAR>(xa, [&](int a) {
+      if constexpr (!FIRST) spread(L::kWLoads, a, [&](int q) { load_w(q); });
+      read_w(t, 1, a);
+    });
+    flush_scales();
+    __builtin_amdgcn_s_waitcnt(MXM_LGKM0);
+    if constexpr (FIRST) vmcnt_le(L::kWLoads + stores);
+    else __builtin_amdgcn_s_waitcnt(MXM_VMCNT(L::kWLoads));
+    wg_barrier();
+    if constexpr (FIRST) issue_tokens(i + 1);
+    next_x();
+    next_w();
+    if constexpr (LAST) {
+      step<2 * PAR + 1>(xb, [&](int a) { spread(L::kXLoads, a, [&](int q) { load_x(rx, q); }); });
+      __builtin_amdgcn_sched_barrier(0);       // the weights' loads stay the youngest
+#pragma unroll
+      for (int q = 0; q < L::kWLoads; ++q) load_w(q);
+    } else {
+      read_x(t + 1, 0, xa);
+      step<2 * PAR + 1>(xb, [&](int a) {
+        spread(L::kXLoads, a, [&](int q) { load_x(rx, q); });
+        read_w(t + 1, 0, a);
+        if constexpr (PAR == 1) read_sw(pr + 1, a);
+      });
+      if constexpr (PAR == 1) read_sx(pr + 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
 
   // One item: its stages and the epilogue.  t: the item's first stage in the
-  // stream; c: its first scale chunk.  A stage's operands are read ahead
-  // within the item; an item's first ones at its start, after the epilogue
-  // before it, whose registers they need.
-  __device__ __forceinline__ void run_item(const Item& it, int i, int t, int c,
+  // stream.  A stage's operands are read ahead within the item; an item's
+  // first ones at its start, after the epilogue before it, whose registers
+  // they need.
+  __device__ __forceinline__ void run_item(const Item& it, int i, int t,
                                            const __amdgpu_buffer_rsrc_t& rx) {
 #pragma unroll
     for (int a = 0; a < AS; ++a)
 #pragma unroll
       for (int m = 0; m < MS; ++m) acc[a][m] = f32x4{0.f, 0.f, 0.f, 0.f};
     {
-      const uint8_t* sc = scales_at(c, 0);
       read_x(t, 0, xa);
-      read_sx(sc, sx);
+      read_sx(0);
 #pragma unroll
       for (int a = 0; a < AS; ++a) {
         read_w(t, 0, a);
-        read_sw(sc, a);
+        read_sw(0, a);
       }
     }
-    for (int s = 0; s + 1 < nst; ++s, ++t) {
-      first_step(t, s, i, rx);
-      const uint8_t* sc = scales_at(c, s + 1);
-      read_x(t + 1, 0, xa);
-      read_sx(sc, sxn);
-      step<1>(xb, [&](int a) {
-        read_w(t + 1, 0, a);
-        read_sw(sc, a);
-      });
-#pragma unroll
-      for (int m = 0; m < MS; ++m) sx[m] = sxn[m];
+    stage<0, true, false>(t, 0, i, rx);
+    const int pairs = nst / 2;
+    for (int pr = 0; pr + 1 < pairs; ++pr) {
+      stage<1, false, false>(t + 2 * pr + 1, pr, i, rx);
+      stage<0, false, false>(t + 2 * pr + 2, pr + 1, i, rx);
     }
-    first_step(t, nst - 1, i, rx);
-    step<1>(xb, [](int) {});
+    stage<1, false, true>(t + nst - 1, pairs - 1, i, rx);
     __builtin_amdgcn_sched_barrier(0);
-    young += epilogue(it);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-
-  // The first step of stage s (t in the stream), the barrier behind which its
-  // slots are free, and the loads that go there.
-  __device__ __forceinline__ void first_step(int t, int s, int i, const __amdgpu_buffer_rsrc_t& rx) {
-    read_x(t, 1, xb);
-    step<0>(xa, [&](int a) { read_w(t, 1, a); });
-    flush_scales();
-    __builtin_amdgcn_s_waitcnt(MXM_LGKM0);
-    vmcnt_le(young);
-    wg_barrier();
-    if (s == 0) issue_tokens(i + 1);
-    issue_x(rx);
-    __builtin_amdgcn_sched_barrier(0);      // the count below is of the loads after these
-    young = issue_w();
+    stores = epilogue(it);
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -538,27 +610,29 @@ struct Tiled {
     cnt = items;
     const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint8_t*>(p.xc), 0, int(int64_t(p.M) * rowb), 0x00020000);
-    issue_tokens(0);
     if constexpr (kGU) {
+      issue_tokens(0);
       __builtin_amdgcn_s_waitcnt(MXM_VMCNT(0));
       wg_barrier();
     }
-    issue_x(rx);
-    flush_scales();
 #pragma unroll
-    for (int q = 0; q < L::kRingW - 1; ++q) issue_w();
-    issue_x(rx);
-    young = issue_w();
-    flush_scales();
+    for (int h = 0; h < kRingX; ++h) {
+      next_x();
+#pragma unroll
+      for (int q = 0; q < L::kXLoads; ++q) load_x(rx, q);
+      flush_scales();
+    }
+#pragma unroll
+    for (int h = 0; h < L::kRingW; ++h) {
+      next_w();
+#pragma unroll
+      for (int q = 0; q < L::kWLoads; ++q) load_w(q);
+    }
     __builtin_amdgcn_s_waitcnt(MXM_LGKM0);
     __builtin_amdgcn_s_waitcnt(MXM_VMCNT(0));
     wg_barrier();
-    int t = 0, c = 0;
-    for (int i = 0; i < cnt; ++i) {
-      run_item(item(i), i, t, c, rx);
-      t += nst;
-      c += (nst + 1) >> 1;
-    }
+    for (int i = 0; i < cnt; ++i) run_item(item(i), i, i * nst, rx);
+    __builtin_amdgcn_s_waitcnt(MXM_VMCNT(0));    // the dead loads past the stream's end
   }
 };
 
@@ -604,12 +678,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_tiled(Problem p) {
       if (lane == 0) mpre[E] = base;
     }
     __syncthreads();
-    const int64_t nitems = int64_t(mpre[E]) * ntn;
+    const int64_t nitems = int64_t(__builtin_amdgcn_readfirstlane(mpre[E])) * ntn;
     const int64_t v0 = nitems * xcd / 8, v1 = nitems * (xcd + 1) / 8;
     // round r's item of this workgroup: ascending when r is even
     auto at = [&](int r) { return v0 + int64_t(r) * gx + ((r & 1) ? gx - 1 - wi : wi); };
     int cnt = 0;
     for (int r = r0; r < r0 + kBatch && v0 + int64_t(r) * gx < v1; ++r) cnt += at(r) < v1;
+    cnt = __builtin_amdgcn_readfirstlane(cnt);
     if (int(threadIdx.x) < cnt) {
       const int64_t v = at(r0 + int(threadIdx.x));
       const int tau = int(v / ntn);
@@ -669,7 +744,7 @@ bool tiled_supported(Kind kind, const Problem& p) {
   const int64_t rowb = p.K / 2;
   if (p.E > kMaxE || int64_t(p.M) * rowb > lim) return false;
   if (int64_t(kind == kGateUp ? p.N + 256 : 256) * rowb > lim) return false;
-  if (int64_t(192) * p.N * 4 > lim) return false;
+  if (int64_t(192) * p.N * 4 > lim || int64_t(p.N) * 2 * (p.K / 32) > lim) return false;
   return kind != kGateUp || p.K > 768;
 }
 
