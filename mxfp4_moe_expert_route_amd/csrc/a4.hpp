@@ -60,11 +60,18 @@ struct Problem {
   int lo, hi;
 };
 
-// Operands straight from memory: every shape.
-hipError_t launch_direct(Kind kind, Out out, const Problem& p, hipStream_t s);
-// Persistent, through LDS.
+// Operands straight from memory: every shape.  Grouped units are low (16 rows;
+// ms 1) or high (64 rows, 32 where h is packed); the product's are 16 cf
+// columns x 16 ms rows: (1, 1), (1, 2), (2, 2) or (2, 4).
+hipError_t launch_direct(Kind kind, Out out, const Problem& p, int ms, hipStream_t s);
+hipError_t launch_direct_gemm(Out out, const Problem& p, int cf, int ms, hipStream_t s);
+// Persistent, through LDS.  Grouped tiles are 32 ms rows tall, ms 1, 2 or 3
+// (split: experts with more rows in a launch of their own, with taller tiles);
+// the product's are 64 as columns x 32 ms rows: (4, 6), (2, 6), (2, 3), (2, 1)
+// or (1, 1).
 bool tiled_supported(Kind kind, const Problem& p);
-hipError_t launch_tiled(Kind kind, Out out, const Problem& p, hipStream_t s);
+hipError_t launch_tiled(Kind kind, Out out, const Problem& p, int ms, bool split, hipStream_t s);
+hipError_t launch_tiled_gemm(Out out, const Problem& p, int as, int ms, hipStream_t s);
 
 }  // namespace a4
 

@@ -3,6 +3,9 @@
 // checks, then launches.  As in api.hip, every check runs before anything is
 // enqueued and none of them touches the HIP runtime.
 #include "../../include/mxfp4moe.h"
+
+#include <cmath>
+
 #include "a4.hpp"
 
 namespace {
@@ -29,11 +32,84 @@ int check_ffn_shape(int T, int H, int I, int E, int k) {
   return MXM_OK;
 }
 
-// Where the contraction runs (decided from sizes alone).
-hipError_t contract(mxm::a4::Kind kind, mxm::a4::Out out, const Problem& p, hipStream_t s) {
-  if (mxm::a4::tiled_supported(kind, p) && (kind != mxm::a4::kGemm || p.M > 16))
-    return mxm::a4::launch_tiled(kind, out, p, s);
-  return mxm::a4::launch_direct(kind, out, p, s);
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Which kernel and tile a product takes: the one whose time, estimated from
+// sizes alone, is least.  A direct unit costs the loads of its fragments, 70
+// ns each per 256 of K and CU; a tiled item the stages of its tile (fits of
+// measured times to about 20%).  In us, 8 x 4096 x 6144: direct (1, 1) 4.8,
+// tiled 64 x 32 11; 333 x 1001 x 2080: direct (2, 4) 6.6, tiled 64 x 32 7.0,
+// 256 x 192 27; 512 x 6144 x 2048: tiled 128 x 192 14, 256 x 192 21, 64 x 32
+// 24; 8192 x 4096 x 6144: 256 x 192 145, 128 x 192 170, 128 x 96 207.
+hipError_t product(mxm::a4::Out out, const Problem& p, hipStream_t s) {
+  struct Tile {
+    int a, ms;
+    double stage, item;                  // tiled: us per stage of 256 of K, per item
+  };
+  constexpr Tile kDirect[] = {{1, 1, 0, 0}, {1, 2, 0, 0}, {2, 2, 0, 0}, {2, 4, 0, 0}};
+  constexpr Tile kTiled[] = {
+      {4, 6, 1.8, 6.0}, {2, 6, 1.15, 3.5}, {2, 3, 0.75, 2.2}, {2, 1, 0.45, 1.2}, {1, 1, 0.33, 1.0}};
+  constexpr int kCus = 256;
+  const double chunks = double(ceil_div(p.K, 256));
+  double best = 1e30;
+  const Tile* t = nullptr;
+  bool tiled = false;
+  for (const Tile& c : kDirect) {
+    const int64_t units = ceil_div(p.N, 16 * c.a) * ceil_div(p.M, 16 * c.ms);
+    const double us = 2.3 + double(ceil_div(units, kCus)) * (0.07 * chunks * (c.a + c.ms) + 0.1);
+    if (us < best) best = us, t = &c;
+  }
+  if (mxm::a4::tiled_supported(mxm::a4::kGemm, p)) {
+    for (const Tile& c : kTiled) {
+      const int64_t items = ceil_div(p.N, 64 * c.a) * ceil_div(p.M, 32 * c.ms);
+      const double us = 3.0 + double(ceil_div(items, kCus)) * (chunks * c.stage + c.item);
+      if (us < best) best = us, t = &c, tiled = true;
+    }
+  }
+  return tiled ? mxm::a4::launch_tiled_gemm(out, p, t->a, t->ms, s)
+               : mxm::a4::launch_direct_gemm(out, p, t->a, t->ms, s);
+}
+
+// The same for the experts' contractions, for a uniform routing.  A row tile is
+// as tall as a typical expert (mean rows and a standard deviation): a taller
+// one multiplies rows that are not there, a shorter one reads the weights
+// again.  Page-shaped gate/up, tiles of 32, 64, 96 and 192 rows: 841, 900, 958,
+// 1154 us at 512 tokens (11 rows an expert); 1372, 933, 1005, 1181 at 2048 (43);
+// 2085, 1483, 1211, 1256 at 4096 (85); 3921, 2217, 1678, 1390 at 8192 (171).
+// Routing is skewed as a rule, so the experts that outgrow the tile go to a
+// taller one in a launch of their own: Zipf-routed, 512 tokens take 525 us so
+// and 637 with 32-row tiles alone.  Where there is nothing for it that launch
+// costs about 4 us: small calls and batches with few rows an expert do without.
+hipError_t grouped(mxm::a4::Kind kind, mxm::a4::Out out, const Problem& p, hipStream_t s) {
+  const bool gu = kind == mxm::a4::kGateUp;
+  const int groups = p.R < p.E ? p.R : p.E;
+  const double mean = double(p.R) / groups;
+  const int64_t tall = int64_t(mean + std::sqrt(mean));
+  const double chunks = double(ceil_div(p.K, 256));
+  constexpr int kCus = 256;
+  double best = 1e30;
+  int ms = 1;
+  bool tiled = false;
+  for (int m = 1; m <= 4; m += 3) {
+    const bool mx = out == mxm::a4::kMx;
+    const int64_t units = groups * ceil_div(tall < 1 ? 1 : tall, mx && m > 1 ? 32 : 16 * m) *
+                          ceil_div(p.N, mx ? 32 : 16);
+    const int frags = (gu ? 2 : 1) * (mx ? 2 : 1) + (mx && m > 1 ? 2 : m);
+    const double us = 2.3 + double(ceil_div(units, kCus)) * (0.07 * chunks * frags + 0.8);
+    if (us < best) best = us, ms = m;
+  }
+  if (mxm::a4::tiled_supported(kind, p)) {
+    constexpr double kStage[] = {1.35, 1.45, 1.5};   // us per stage of 256 of K
+    for (int m = 1; m <= 3; ++m) {
+      const int64_t items = groups * ceil_div(tall < 1 ? 1 : tall, 32 * m) * ceil_div(p.N, gu ? 128 : 256);
+      const double us = 3.0 + double(ceil_div(items, kCus)) * (chunks * kStage[m - 1] + 1.2 * m);
+      if (us < best) best = us, ms = m, tiled = true;
+    }
+  }
+  if (!tiled) return mxm::a4::launch_direct(kind, out, p, ms, s);
+  const bool split = mean >= 4 && best > 60;
+  if (split) ms = tall <= 32 ? 1 : tall <= 64 ? 2 : 3;
+  return mxm::a4::launch_tiled(kind, out, p, ms, split, s);
 }
 
 }  // namespace
@@ -53,8 +129,8 @@ int mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b
   p.out = c;
   p.M = M; p.R = M; p.N = N; p.K = K; p.E = 1; p.k = 1;
   p.lo = 1; p.hi = INT32_MAX;
-  return launched(contract(mxm::a4::kGemm, c_dtype == MXM_F32 ? mxm::a4::kF32 : mxm::a4::kBf16, p,
-                           as_stream(stream)));
+  return launched(product(c_dtype == MXM_F32 ? mxm::a4::kF32 : mxm::a4::kBf16, p,
+                          as_stream(stream)));
 }
 
 int moe_mxfp4_a4_gate_up_swiglu(const uint8_t* x_codes, const uint8_t* x_scales,
@@ -78,8 +154,8 @@ int moe_mxfp4_a4_gate_up_swiglu(const uint8_t* x_codes, const uint8_t* x_scales,
   p.out = h_bf16; p.oc = h_codes; p.os = h_scales;
   p.M = T; p.R = T * k; p.N = I; p.K = H; p.E = E; p.k = k;
   p.lo = 1; p.hi = INT32_MAX;
-  return launched(contract(mxm::a4::kGateUp, mx ? mxm::a4::kMx : mxm::a4::kBf16, p,
-                           as_stream(stream)));
+  return launched(grouped(mxm::a4::kGateUp, mx ? mxm::a4::kMx : mxm::a4::kBf16, p,
+                          as_stream(stream)));
 }
 
 int moe_mxfp4_a4_down(const uint8_t* h_codes, const uint8_t* h_scales, const int32_t* offsets,
@@ -97,7 +173,7 @@ int moe_mxfp4_a4_down(const uint8_t* h_codes, const uint8_t* h_scales, const int
   p.out = y;
   p.M = T * k; p.R = T * k; p.N = H; p.K = I; p.E = E; p.k = k;
   p.lo = 1; p.hi = INT32_MAX;
-  return launched(contract(mxm::a4::kDown, mxm::a4::kF32, p, as_stream(stream)));
+  return launched(grouped(mxm::a4::kDown, mxm::a4::kF32, p, as_stream(stream)));
 }
 
 int moe_mxfp4_a4_layer(const uint16_t* x_bf16, const float* logits, int T, int H, int I, int E,

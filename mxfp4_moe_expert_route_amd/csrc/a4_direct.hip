@@ -227,24 +227,23 @@ hipError_t launch(const Problem& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <Kind KIND, Out OUT, int CF>
-hipError_t launch_rows(const Problem& p, hipStream_t s) {
-  const int groups = KIND == kGemm || p.R < p.E ? 1 : p.E;
-  const int mean = (KIND == kGemm ? p.M : p.R) / groups;
-  if (mean <= 16) return launch<KIND, OUT, CF, 1>(p, s);
-  return launch<KIND, OUT, CF, 4>(p, s);
+template <Out OUT>
+hipError_t launch_gemm(const Problem& p, int cf, int ms, hipStream_t s) {
+  if (cf == 1) return ms == 1 ? launch<kGemm, OUT, 1, 1>(p, s) : launch<kGemm, OUT, 1, 2>(p, s);
+  return ms == 2 ? launch<kGemm, OUT, 2, 2>(p, s) : launch<kGemm, OUT, 2, 4>(p, s);
 }
 
 }  // namespace
 
-hipError_t launch_direct(Kind kind, Out out, const Problem& p, hipStream_t s) {
-  if (kind == kGemm) {
-    if (out == kBf16) return launch_rows<kGemm, kBf16, 1>(p, s);
-    return launch_rows<kGemm, kF32, 1>(p, s);
-  }
-  if (kind == kDown) return launch_rows<kDown, kF32, 1>(p, s);
-  if (out == kMx) return launch<kGateUp, kMx, 2, 1>(p, s);
-  return launch_rows<kGateUp, kBf16, 1>(p, s);
+hipError_t launch_direct(Kind kind, Out out, const Problem& p, int ms, hipStream_t s) {
+  if (kind == kDown) return ms == 1 ? launch<kDown, kF32, 1, 1>(p, s) : launch<kDown, kF32, 1, 4>(p, s);
+  if (out == kMx)
+    return ms == 1 ? launch<kGateUp, kMx, 2, 1>(p, s) : launch<kGateUp, kMx, 2, 2>(p, s);
+  return ms == 1 ? launch<kGateUp, kBf16, 1, 1>(p, s) : launch<kGateUp, kBf16, 1, 4>(p, s);
+}
+
+hipError_t launch_direct_gemm(Out out, const Problem& p, int cf, int ms, hipStream_t s) {
+  return out == kBf16 ? launch_gemm<kBf16>(p, cf, ms, s) : launch_gemm<kF32>(p, cf, ms, s);
 }
 
 }  // namespace a4

@@ -49,7 +49,7 @@ constexpr uint32_t kDead = 0x80000000u;       // a buffer offset out of every ra
 
 template <int AS, int MS>
 struct Lds {
-  static constexpr int kNT = 64 * AS;                        // weight rows per n-tile
+  static constexpr int kNT = 16 * kWN * AS;                 // weight rows per n-tile
   static constexpr int kMT = 16 * kWM * MS;                  // rows per m-tile, at most
   static constexpr int kWSlot = kNT * 128;
   static constexpr int kXSlot = kMT * 128;
@@ -733,6 +733,38 @@ hipError_t launch_k(const Problem& p, hipStream_t s) {
   return whole ? launch<KIND, OUT, AS, MS, true>(p, s) : launch<KIND, OUT, AS, MS, false>(p, s);
 }
 
+// Experts of up to 32 LIGHT rows with tiles as tall, the others with tiles of
+// 32 HEAVY rows.
+template <Kind KIND, Out OUT, int LIGHT, int HEAVY>
+hipError_t launch_split(const Problem& p, hipStream_t s) {
+  Problem part = p;
+  part.lo = 32 * LIGHT + 1;
+  const hipError_t e = launch_k<KIND, OUT, 4, HEAVY>(part, s);
+  if (e != hipSuccess) return e;
+  part.lo = p.lo;
+  part.hi = 32 * LIGHT + 1;
+  return launch_k<KIND, OUT, 4, LIGHT>(part, s);
+}
+
+template <Kind KIND, Out OUT>
+hipError_t launch_grouped(const Problem& p, int ms, bool split, hipStream_t s) {
+  if (split) {
+    if (ms == 1) return launch_split<KIND, OUT, 1, 3>(p, s);
+    return ms == 2 ? launch_split<KIND, OUT, 2, 6>(p, s) : launch_split<KIND, OUT, 3, 6>(p, s);
+  }
+  if (ms == 1) return launch_k<KIND, OUT, 4, 1>(p, s);
+  return ms == 2 ? launch_k<KIND, OUT, 4, 2>(p, s) : launch_k<KIND, OUT, 4, 3>(p, s);
+}
+
+template <Out OUT>
+hipError_t launch_gemm(const Problem& p, int as, int ms, hipStream_t s) {
+  if (as == 4) return launch_k<kGemm, OUT, 4, 6>(p, s);
+  if (as == 1) return launch_k<kGemm, OUT, 1, 1>(p, s);
+  if (ms == 6) return launch_k<kGemm, OUT, 2, 6>(p, s);
+  if (ms == 3) return launch_k<kGemm, OUT, 2, 3>(p, s);
+  return launch_k<kGemm, OUT, 2, 1>(p, s);
+}
+
 }  // namespace
 
 // The kernel addresses activations and one item's weights and outputs by
@@ -748,19 +780,14 @@ bool tiled_supported(Kind kind, const Problem& p) {
   return kind != kGateUp || p.K > 768;
 }
 
-hipError_t launch_tiled(Kind kind, Out out, const Problem& p, hipStream_t s) {
-  const int groups = kind == kGemm || p.R < p.E ? (kind == kGemm ? 1 : p.R) : p.E;
-  const int mean = p.R / groups;
-  if (mean <= 24) {
-    if (kind == kGemm)
-      return out == kBf16 ? launch_k<kGemm, kBf16, 4, 1>(p, s) : launch_k<kGemm, kF32, 4, 1>(p, s);
-    if (kind == kDown) return launch_k<kDown, kF32, 4, 1>(p, s);
-    return out == kMx ? launch_k<kGateUp, kMx, 4, 1>(p, s) : launch_k<kGateUp, kBf16, 4, 1>(p, s);
-  }
-  if (kind == kGemm)
-    return out == kBf16 ? launch_k<kGemm, kBf16, 4, 6>(p, s) : launch_k<kGemm, kF32, 4, 6>(p, s);
-  if (kind == kDown) return launch_k<kDown, kF32, 4, 6>(p, s);
-  return out == kMx ? launch_k<kGateUp, kMx, 4, 6>(p, s) : launch_k<kGateUp, kBf16, 4, 6>(p, s);
+hipError_t launch_tiled(Kind kind, Out out, const Problem& p, int ms, bool split, hipStream_t s) {
+  if (kind == kDown) return launch_grouped<kDown, kF32>(p, ms, split, s);
+  return out == kMx ? launch_grouped<kGateUp, kMx>(p, ms, split, s)
+                    : launch_grouped<kGateUp, kBf16>(p, ms, split, s);
+}
+
+hipError_t launch_tiled_gemm(Out out, const Problem& p, int as, int ms, hipStream_t s) {
+  return out == kBf16 ? launch_gemm<kBf16>(p, as, ms, s) : launch_gemm<kF32>(p, as, ms, s);
 }
 
 }  // namespace a4
