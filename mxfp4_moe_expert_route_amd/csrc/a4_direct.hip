@@ -2,12 +2,14 @@
 // operands from memory straight into the registers of the scaled matrix
 // instructions.  Takes every shape.
 //
-// A workgroup's unit is 16 CF output columns x 16 MS rows over the whole of
-// K.  Its waves deal the 256-element chunks of K among themselves (a chunk is
-// one 128-byte line of codes per row) and their partial sums meet in LDS,
-// added in wave order, so results do not depend on timing.  Splitting K
-// rather than the columns keeps every byte of a unit in flight at once: with
-// few rows the cost is the latency of the weight bytes, not their number.
+// A unit is 16 CF output columns x 16 MS rows over the whole of K.  Where K is
+// long (SPLIT) a workgroup's eight waves deal its 256-element chunks (a chunk
+// is one 128-byte line of codes per row) among themselves and their partial
+// sums meet in LDS, added in wave order, so results do not depend on timing:
+// splitting K rather than the columns keeps every byte of a unit in flight at
+// once, and with few rows the cost is the latency of the weight bytes, not
+// their number (8 x 4096 x 6144: 4.8 us for 12.6 MB).  Where K is a few chunks,
+// each wave has a unit to itself.
 #include "a4.hpp"
 #include "mx_pack.hpp"
 
@@ -18,12 +20,27 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kChunkBlocks = 8;                // MX blocks per chunk (256 of K)
+// K in one chunk is one wave's work; up to four are where there are units for
+// half the waves the GPU holds (a long K goes faster split, 2785 x 29 x 544 in
+// 3.2 instead of 5.6 us; many short units alone, 1272 x 2927 x 192 in 7.4
+// instead of 20)
+constexpr int kAloneChunks = 4;
+constexpr int kAloneUnits = 1024;
 
 template <bool LINES>
 struct Frag {
   uint4 c[2];            // this lane's blocks g and 4 + g of the chunk
   uint32_t s[2];         // and their scale bytes
 };
+
+// Store at an address aligned to its elements alone (a row may start anywhere).
+template <class T>
+__device__ __forceinline__ void store_any(void* p, const T& v) {
+  struct __attribute__((packed, aligned(2))) U {
+    T v;
+  };
+  static_cast<U*>(p)->v = v;
+}
 
 // Chunk `ch` of the row at (codes, scales).  LINES: K is whole chunks and the
 // scale rows are 8-byte aligned.  Blocks past the end of K load as zeros under
@@ -56,10 +73,10 @@ __device__ __forceinline__ Frag<LINES> load_frag(const uint8_t* codes, const uin
 }
 
 // CF: 16-column groups per unit; MS: 16-row groups per unit.
-template <Kind KIND, Out OUT, int CF, int MS, bool LINES>
+template <Kind KIND, Out OUT, int CF, int MS, bool LINES, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void k_direct(Problem p) {
   constexpr int WF = KIND == kGateUp ? 2 * CF : CF;        // weight fragments
-  __shared__ f32x4 part[kWaves][WF * MS][kWave];
+  __shared__ f32x4 part[SPLIT ? kWaves : 1][SPLIT ? WF * MS : 1][kWave];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = lane_id();
   const int r16 = lane & 15, g = lane >> 4;
@@ -68,7 +85,9 @@ __global__ __launch_bounds__(kThreads) void k_direct(Problem p) {
   const int nch = (nblk + kChunkBlocks - 1) / kChunkBlocks;
   const int ncol = (p.N + 16 * CF - 1) / (16 * CF);
 
-  for (int64_t slot = blockIdx.x;; slot += gridDim.x) {
+  const int64_t first = SPLIT ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * kWaves + wave;
+  const int64_t stride = SPLIT ? int64_t(gridDim.x) : int64_t(gridDim.x) * kWaves;
+  for (int64_t slot = first;; slot += stride) {
     const int tau = int(slot / ncol);
     const int n0 = int(slot - int64_t(tau) * ncol) * 16 * CF;
     Tile t;
@@ -106,7 +125,7 @@ __global__ __launch_bounds__(kThreads) void k_direct(Problem p) {
     for (int a = 0; a < WF; ++a)
 #pragma unroll
       for (int m = 0; m < MS; ++m) acc[a][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int ch = wave; ch < nch; ch += kWaves) {
+    for (int ch = SPLIT ? wave : 0; ch < nch; ch += SPLIT ? kWaves : 1) {
       Frag<LINES> w[WF], x[MS];
 #pragma unroll
       for (int a = 0; a < WF; ++a) w[a] = load_frag<LINES>(wc[a], ws[a], ch, nblk);
@@ -120,21 +139,29 @@ __global__ __launch_bounds__(kThreads) void k_direct(Problem p) {
           for (int m = 0; m < MS; ++m)
             acc[a][m] = mfma(w[a].c[h], w[a].s[h], x[m].c[h], x[m].s[h], acc[a][m]);
     }
+    if constexpr (SPLIT) {
 #pragma unroll
-    for (int a = 0; a < WF; ++a)
+      for (int a = 0; a < WF; ++a)
 #pragma unroll
-      for (int m = 0; m < MS; ++m) part[wave][a * MS + m][lane] = acc[a][m];
-    __syncthreads();
+        for (int m = 0; m < MS; ++m) part[wave][a * MS + m][lane] = acc[a][m];
+      __syncthreads();
+    }
 
-    // the row groups' sums are dealt over the waves; lane: columns 4g .. 4g+3
-    // of row r16
+    // lane: columns 4g .. 4g+3 of row r16; a split unit's row groups are dealt
+    // over the waves
     auto total = [&](int a, int m) {
-      f32x4 v = part[0][a * MS + m][lane];
+      if constexpr (SPLIT) {
+        f32x4 v = part[0][a * MS + m][lane];
 #pragma unroll
-      for (int q = 1; q < kWaves; ++q) v += part[q][a * MS + m][lane];
-      return v;
+        for (int q = 1; q < kWaves; ++q) v += part[q][a * MS + m][lane];
+        return v;
+      } else {
+        return acc[a][m];
+      }
     };
-    for (int m = wave; m < MS; m += kWaves) {
+#pragma unroll
+    for (int m = 0; m < MS; ++m) {
+      if (SPLIT && m % kWaves != wave) continue;
       const int64_t row = int64_t(t.row0) + 16 * m + r16;
       const bool live = 16 * m + r16 < t.rows;
       if constexpr (OUT == kMx) {
@@ -179,12 +206,10 @@ __global__ __launch_bounds__(kThreads) void k_direct(Problem p) {
           }
           if (!live) continue;
           const int n = n0 + 16 * a + 4 * g;
-          // rows of 4 n columns start on whole 16 (8) bytes; others are
-          // written one by one
           if constexpr (OUT == kF32) {
             float* o = static_cast<float*>(p.out) + row * p.N + n;
-            if (n + 4 <= p.N && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
-              *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+            if (n + 4 <= p.N) {
+              store_any(o, v);
             } else {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -195,8 +220,8 @@ __global__ __launch_bounds__(kThreads) void k_direct(Problem p) {
             uint32_t b[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) b[i] = f32_to_bf16_rne(v[i]);
-            if (n + 4 <= p.N && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
-              *reinterpret_cast<uint2*>(o) = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+            if (n + 4 <= p.N) {
+              store_any(o, make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16)));
             } else {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -206,7 +231,7 @@ __global__ __launch_bounds__(kThreads) void k_direct(Problem p) {
         }
       }
     }
-    __syncthreads();                 // the sums are read: LDS is free
+    if constexpr (SPLIT) __syncthreads();      // the sums are read: LDS is free
   }
 }
 
@@ -219,11 +244,19 @@ hipError_t launch(const Problem& p, hipStream_t s) {
   const int64_t full = p.R / (16 * MS);
   const int64_t tiles = KIND == kGemm ? (int64_t(p.M) + 16 * MS - 1) / (16 * MS)
                                       : full + (p.R < p.E ? p.R : p.E);
-  const int64_t cap = int64_t(device_cus()) * 4;
   const int64_t slots = tiles * ncol;
-  const unsigned grid = unsigned(slots < cap ? slots : cap);
-  if (lines) k_direct<KIND, OUT, CF, MS, true><<<grid, kThreads, 0, s>>>(p);
-  else k_direct<KIND, OUT, CF, MS, false><<<grid, kThreads, 0, s>>>(p);
+  const int64_t chunks = (p.K + 255) / 256;
+  const bool split = chunks > kAloneChunks || (chunks > 1 && slots <= kAloneUnits);
+  const int64_t groups = split ? slots : (slots + kWaves - 1) / kWaves;
+  const int64_t cap = int64_t(device_cus()) * 4;
+  const unsigned grid = unsigned(groups < cap ? groups : cap);
+  if (split) {
+    if (lines) k_direct<KIND, OUT, CF, MS, true, true><<<grid, kThreads, 0, s>>>(p);
+    else k_direct<KIND, OUT, CF, MS, false, true><<<grid, kThreads, 0, s>>>(p);
+  } else {
+    if (lines) k_direct<KIND, OUT, CF, MS, true, false><<<grid, kThreads, 0, s>>>(p);
+    else k_direct<KIND, OUT, CF, MS, false, false><<<grid, kThreads, 0, s>>>(p);
+  }
   return hipGetLastError();
 }
 

@@ -294,15 +294,31 @@ struct Tiled {
         // a half past the row's end is not used; it reads the row's first
         spend[h] = *reinterpret_cast<const u32x4*>(src + (b0 < nblk ? b0 : 0));
       } else {
+        // sixteen bytes from anywhere, if the scales go on that far; blocks
+        // past the row's end get scale 1
+        const uint8_t* end = sload_w(h) ? p.ws + erow(p.E) * nblk : p.xs + int64_t(p.M) * nblk;
+        if (src + b0 + 16 <= end) {
+          struct __attribute__((packed, aligned(1))) U {
+            u32x4 v;
+          };
+          spend[h] = reinterpret_cast<const U*>(src + b0)->v;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          uint32_t v = 0;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int blk = b0 + 4 * d + b;
-            v |= (blk < nblk ? uint32_t(src[blk]) : 127u) << (8 * b);
+          for (int d = 0; d < 4; ++d) {
+            const int in = min(max(nblk - b0 - 4 * d, 0), 4);      // bytes inside the row
+            const uint32_t keep = in == 4 ? 0xffffffffu : (1u << (8 * in)) - 1u;
+            spend[h][d] = (spend[h][d] & keep) | (0x7f7f7f7fu & ~keep);
           }
-          spend[h][d] = v;
+        } else {
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            uint32_t v = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const int blk = b0 + 4 * d + b;
+              v |= (blk < nblk ? uint32_t(src[blk]) : 127u) << (8 * b);
+            }
+            spend[h][d] = v;
+          }
         }
       }
     }
@@ -489,8 +505,10 @@ struct Tiled {
       uint8_t* base = static_cast<uint8_t*>(p.out) + row0 * p.N * kSize;
       const __amdgpu_buffer_rsrc_t ro =
           __builtin_amdgcn_make_buffer_rsrc(base, 0, 0x7fffffff, 0x00020000);
-      // rows of whole vectors, or elements one by one
-      const bool vec = p.N % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & (4 * kSize - 1)) == 0;
+      // four columns a store, wherever their row starts (buffer stores need
+      // no alignment); the last columns of an N that is no multiple of four
+      // one by one
+      const bool edge = p.N % 4 != 0 && (it.n + 1) * kCols >= p.N;
 #pragma unroll
       for (int i = 0; i < MS; ++i) {
         const int j = 16 * (wm + kWM * i) + r16;
@@ -506,28 +524,28 @@ struct Tiled {
           const int col = col0 + 16 * a;
           const uint32_t at = (uint32_t(j) * uint32_t(p.N) + uint32_t(col)) * kSize;
           const bool live = j < it.rows;
+          const uint32_t to = live && col + 4 <= p.N ? at : kDead;
           if constexpr (OUT == kF32) {
-            const u32x4 b = __builtin_bit_cast(u32x4, v);
-            if (vec) {
-              __builtin_amdgcn_raw_buffer_store_b128(b, ro, live && col < p.N ? at : kDead, 0, 0);
-            } else {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ro, to, 0, 0);
+            if (edge) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                __builtin_amdgcn_raw_buffer_store_b32(b[c], ro, live && col + c < p.N ? at + 4 * c : kDead,
-                                                      0, 0);
+              for (int c = 0; c < 3; ++c)
+                __builtin_amdgcn_raw_buffer_store_b32(
+                    __builtin_bit_cast(uint32_t, v[c]), ro,
+                    live && col + 4 > p.N && col + c < p.N ? at + 4 * c : kDead, 0, 0);
             }
           } else {
             uint32_t b[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) b[c] = f32_to_bf16_rne(v[c]);
-            if (vec) {
-              __builtin_amdgcn_raw_buffer_store_b64(u32x2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)}, ro,
-                                                        live && col < p.N ? at : kDead, 0, 0);
-            } else {
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)}, ro, to,
+                                                  0, 0);
+            if (edge) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                __builtin_amdgcn_raw_buffer_store_b16(uint16_t(b[c]), ro,
-                                                          live && col + c < p.N ? at + 2 * c : kDead, 0, 0);
+              for (int c = 0; c < 3; ++c)
+                __builtin_amdgcn_raw_buffer_store_b16(
+                    uint16_t(b[c]), ro, live && col + 4 > p.N && col + c < p.N ? at + 2 * c : kDead, 0,
+                    0);
             }
           }
           n += 1;                            // at least

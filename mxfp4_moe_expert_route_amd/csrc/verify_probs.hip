@@ -15,11 +15,12 @@
 // boundary.  Sums run in a fixed order.
 //
 // Of the (L + 1) V probabilities of a block only the drafted tokens' entries
-// and the two rows at position n are read.  A row is cut into parts, one
-// wave's sum each; the draw finds the part that holds it and reads that one
-// again.  A small vocabulary (or a batch that fills the CUs by itself) takes
-// one launch, a workgroup per block.  A large one takes two, since fp64 sums
-// over 152064 tokens keep one CU busy for about 16 us: the parts' sums by
+// and the two rows at position n are read.  Up to 8192 tokens a workgroup per
+// block does it all, with its threads' weights in registers.  Beyond that a row
+// is cut into parts, one wave's sum each; the draw finds the part that holds it
+// and reads that one again.  A batch that fills the CUs by itself takes one
+// launch for that, a workgroup per block; a smaller one takes two, since fp64
+// sums over 152064 tokens keep one CU busy for about 16 us: the parts' sums by
 // workgroups that each find n themselves (2 L loads, cheaper than a launch),
 // then the draw.
 #include "a4.hpp"
@@ -31,10 +32,10 @@ constexpr int kSplitT = 256;                   // threads of a summing workgroup
 constexpr int kDrawT = 512;
 constexpr int kOneT = 1024;                    // threads where one workgroup does it all
 constexpr int kMaxParts = 256;
-constexpr int kOneV = 16384;                   // vocabulary one workgroup sums in about 2 us
+constexpr int kOwn = 8;                        // weights a thread holds in registers
 constexpr int kOneB = 512;                     // blocks that fill the CUs by themselves
 
-bool one_launch(int B, int V) { return V <= kOneV || B >= kOneB; }
+bool one_launch(int B, int V) { return V <= kOneT * kOwn || B >= kOneB; }
 
 // Parts per row where two launches are taken: about eight waves a CU, at
 // least 512 tokens a wave.
@@ -145,18 +146,18 @@ struct Block {
         tokens(tok + int64_t(b) * L_), u(uni + int64_t(b) * (L_ + 1)),
         len(draft_len ? min(max(draft_len[b], 0), L_) : L_), L(L_), V(V_) {}
 
-  // Accepted tokens (every wave computes it; uniform result).
+  // Accepted tokens (every wave computes it; uniform result).  The loads do
+  // not wait for the block's length.
   __device__ __forceinline__ int accepted() const {
     const int lane = lane_id();
     bool fail = false;
-    if (lane < len) {
+    if (lane < L) {
       const int d = tokens[lane];
-      fail = true;
-      if (d >= 0 && d < V) {
-        const double pd = clean(value(target, int64_t(lane) * V + d));
-        const double qd = clean(value(draft, int64_t(lane) * V + d));
-        fail = !(double(u[lane]) * qd < pd);
-      }
+      const float ui = u[lane];
+      const bool inside = d >= 0 && d < V;
+      const int64_t at = int64_t(lane) * V + (inside ? d : 0);
+      const double pd = clean(value(target, at)), qd = clean(value(draft, at));
+      fail = lane < len && !(inside && double(ui) * qd < pd);
     }
     const unsigned long long m = __ballot(fail);
     return __builtin_amdgcn_readfirstlane(m ? __ffsll((long long)m) - 1 : len);
@@ -324,6 +325,71 @@ __global__ __launch_bounds__(kOneT) void k_vp_one(
   if (threadIdx.x == 0) accept_len[b] = n;
 }
 
+// One workgroup per block and at most kOwn tokens per thread: thread t owns a
+// run of them, so thread order is token order and one prefix sum finds the
+// draw.
+template <int NT, class T>
+__global__ __launch_bounds__(NT) void k_vp_own(
+    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
+    const int32_t* __restrict__ draft_len, const float* __restrict__ uniforms, int L, int V,
+    int each, int32_t* __restrict__ accept_len, int32_t* __restrict__ next_token) {
+  __shared__ double tot[NT / kWave];
+  __shared__ unsigned long long mask[2 * (NT / kWave)];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const Block<T> blk(target, draft, tokens, draft_len, uniforms, b, L, V);
+  const float u = blk.u[L];
+  const int n = blk.accepted();
+  const T* p = blk.p(n);
+  const T* q = blk.q(n);
+  const int a0 = min(tid * each, V), own = min(each, V - a0);
+  float pv[kOwn], qv[kOwn];
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    pv[k] = qv[k] = 0.f;
+    if (k < own) {
+      pv[k] = value(p, a0 + k);
+      if (q) qv[k] = value(q, a0 + k);
+    }
+  }
+  if (tid == 0) accept_len[b] = n;
+  bool residual = q != nullptr;
+  for (;;) {
+    double w[kOwn], run = 0.0;
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      w[k] = weight(pv[k], residual ? qv[k] : 0.f);
+      run += w[k];
+    }
+    const double incl = block_prefix<NT>(run, tot);
+    double total = 0.0;
+#pragma unroll
+    for (int k = 0; k < NT / kWave; ++k) total += tot[k];
+    if (!(total > 0.0)) {
+      if (!residual) {                         // no token has probability
+        if (tid == 0) next_token[b] = -1;
+        return;
+      }
+      residual = false;                        // no difference: from p itself
+      continue;
+    }
+    const double goal = double(u) * total;
+    const int c = claim<NT>(run > 0.0 && goal < incl, run > 0.0, mask);
+    if (tid == c) {
+      int found = -1;
+      double at = incl - run;
+#pragma unroll
+      for (int k = 0; k < kOwn; ++k) {
+        if (w[k] > 0.0 && (found < 0 || !(at > goal))) {
+          found = a0 + k;
+          at += w[k];
+        }
+      }
+      next_token[b] = found;
+    }
+    return;
+  }
+}
+
 template <class T>
 hipError_t launch_typed(const void* target, const void* draft, const int32_t* tokens,
                         const int32_t* draft_len, const float* uniforms, int B, int L, int V,
@@ -332,6 +398,17 @@ hipError_t launch_typed(const void* target, const void* draft, const int32_t* to
   const T* q = static_cast<const T*>(draft);
   const bool vec = V % (16 / int(sizeof(T))) == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 &&
                    reinterpret_cast<uintptr_t>(q) % 16 == 0;
+  if (V <= kSplitT * kOwn) {
+    k_vp_own<kSplitT, T><<<unsigned(B), kSplitT, 0, s>>>(p, q, tokens, draft_len, uniforms, L, V,
+                                                         (V + kSplitT - 1) / kSplitT, accept_len,
+                                                         next_token);
+    return hipGetLastError();
+  }
+  if (V <= kOneT * kOwn) {
+    k_vp_own<kOneT, T><<<unsigned(B), kOneT, 0, s>>>(p, q, tokens, draft_len, uniforms, L, V,
+                                                     (V + kOneT - 1) / kOneT, accept_len, next_token);
+    return hipGetLastError();
+  }
   if (one_launch(B, V)) {
     k_vp_one<T><<<unsigned(B), kOneT, 0, s>>>(p, q, tokens, draft_len, uniforms, L, V,
                                               span_of(V, kOneT / kWave), vec, accept_len, next_token);

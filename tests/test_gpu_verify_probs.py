@@ -58,7 +58,8 @@ def check(mm, p, q, tokens, u, lengths, dtype):
 
 SIZES = [(1, 1, 1), (3, 2, 2), (5, 1, 3), (7, 8, 64), (4, 32, 100), (2, 8, 1000), (70, 3, 257), (6, 8, 1024),
          (3, 8, 5001), (9, 5, 20011), (600, 2, 300), (2, 8, 152064), (1, 2, 16385), (130, 1, 17001), (1, 1, 65536),
-         (513, 1, 17000)]
+         (513, 1, 17000),
+         (4, 3, 2048), (4, 3, 2049), (5, 2, 8192), (5, 2, 8193), (520, 1, 8200)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
@@ -73,7 +74,7 @@ def test_matches_oracle(mm, B, L, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
-@pytest.mark.parametrize("V", [5, 300, 4099, 20000])
+@pytest.mark.parametrize("V", [5, 300, 2049, 4099, 8300, 20000])
 def test_edges(mm, V, dtype):
     say("verify_probs edges", V, dtype)
     rng = np.random.default_rng(V)
