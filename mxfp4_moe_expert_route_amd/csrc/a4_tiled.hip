@@ -294,32 +294,11 @@ struct Tiled {
         // a half past the row's end is not used; it reads the row's first
         spend[h] = *reinterpret_cast<const u32x4*>(src + (b0 < nblk ? b0 : 0));
       } else {
-        // sixteen bytes from anywhere, if the scales go on that far; blocks
-        // past the row's end get scale 1
-        const uint8_t* end = sload_w(h) ? p.ws + erow(p.E) * nblk : p.xs + int64_t(p.M) * nblk;
-        if (src + b0 + 16 <= end) {
-          struct __attribute__((packed, aligned(1))) U {
-            u32x4 v;
-          };
-          spend[h] = reinterpret_cast<const U*>(src + b0)->v;
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const int in = min(max(nblk - b0 - 4 * d, 0), 4);      // bytes inside the row
-            const uint32_t keep = in == 4 ? 0xffffffffu : (1u << (8 * in)) - 1u;
-            spend[h][d] = (spend[h][d] & keep) | (0x7f7f7f7fu & ~keep);
-          }
-        } else {
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            uint32_t v = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const int blk = b0 + 4 * d + b;
-              v |= (blk < nblk ? uint32_t(src[blk]) : 127u) << (8 * b);
-            }
-            spend[h][d] = v;
-          }
-        }
+        // sixteen bytes from any address, the row's last at the latest
+        struct __attribute__((packed, aligned(1))) U {
+          u32x4 v;
+        };
+        spend[h] = reinterpret_cast<const U*>(src + min(b0, nblk - 16))->v;
       }
     }
     sfull = true;
@@ -328,10 +307,24 @@ struct Tiled {
     if (sfull) {
 #pragma unroll
       for (int h = 0; h < L::kSLoads; ++h)
-        if (sload_any(h))
-          *reinterpret_cast<u32x4*>(lds + L::kS + 1024 * sload(h) + 16 * lane) = transpose4(spend[h]);
+        if (sload_any(h)) {
+          *reinterpret_cast<u32x4*>(lds + L::kS + 1024 * sload(h) + 16 * lane) =
+              transpose4(WHOLE ? spend[h] : trim_scales(spend[h]));
+        }
     }
     sfull = false;
+  }
+  // Scales loaded from the row's last sixteen blocks move to their places.
+  // (xs is one past the stage of the load.)
+  __device__ __forceinline__ u32x4 trim_scales(u32x4 v) {
+    const int lane = lane_here();
+    const int by = max(8 * ((xs - 1) & ~3) + 16 * ((lane & 1) ^ ((lane >> 4) & 1)) + 16 - nblk, 0);
+    if (by & 8) v.x = v.z, v.y = v.w;
+    if (by & 4) v.x = v.y, v.y = v.z, v.z = v.w;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      v[d] = __builtin_amdgcn_alignbyte(d < 3 ? v[d + 1] : 0u, v[d], uint32_t(by) & 3u);
+    return v;
   }
 
   // Next stage of the activation stream: where it goes; a new item's rows; new
@@ -348,7 +341,13 @@ struct Tiled {
     }
     if (xs == 0) x_item();
     if ((xs & 3) == 0) load_scales();
-    if (!WHOLE && 8 * xs + int((lane & 7) ^ (lane >> 3)) >= nblk) xtail = kDead;
+    if (!WHOLE && 8 * xs + 8 > nblk) {
+      // an item's last stages: pieces past the row's end are dead from here on
+      const int lane = lane_here();
+      const uint32_t dead = 8 * xs + ((lane & 7) ^ (lane >> 3)) >= nblk ? kDead : 0u;
+#pragma unroll
+      for (int q = 0; q < L::kXLoads; ++q) xoff[q] |= dead;
+    }
     if (++xs == nst) {
       xs = 0;
       ++xi;
@@ -744,11 +743,14 @@ hipError_t launch(const Problem& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Where K is not whole, 192 rows of gate/up leave no registers to bring scales
+// to their places (spills in the main loop); 160 do.
 template <Kind KIND, Out OUT, int AS, int MS>
 hipError_t launch_k(const Problem& p, hipStream_t s) {
   const bool whole = p.K % 512 == 0 && reinterpret_cast<uintptr_t>(p.xs) % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(p.ws) % 16 == 0;
-  return whole ? launch<KIND, OUT, AS, MS, true>(p, s) : launch<KIND, OUT, AS, MS, false>(p, s);
+  constexpr int kRest = KIND == kGateUp && MS == 6 ? 5 : MS;
+  return whole ? launch<KIND, OUT, AS, MS, true>(p, s) : launch<KIND, OUT, AS, kRest, false>(p, s);
 }
 
 // Experts of up to 32 LIGHT rows with tiles as tall, the others with tiles of
@@ -788,14 +790,14 @@ hipError_t launch_gemm(const Problem& p, int as, int ms, hipStream_t s) {
 // The kernel addresses activations and one item's weights and outputs by
 // 31-bit byte offsets.  The pair ids of a gate/up item are fetched while the
 // item before it runs its first stage and used two stages before its last:
-// four stages.
+// four stages.  Scales are loaded 16 blocks of a row at a time: K >= 512.
 bool tiled_supported(Kind kind, const Problem& p) {
   const int64_t lim = (int64_t(1) << 31) - 1;
   const int64_t rowb = p.K / 2;
   if (p.E > kMaxE || int64_t(p.M) * rowb > lim) return false;
   if (int64_t(kind == kGateUp ? p.N + 256 : 256) * rowb > lim) return false;
   if (int64_t(192) * p.N * 4 > lim || int64_t(p.N) * 2 * (p.K / 32) > lim) return false;
-  return kind != kGateUp || p.K > 768;
+  return p.K >= (kind == kGateUp ? 800 : 512);
 }
 
 hipError_t launch_tiled(Kind kind, Out out, const Problem& p, int ms, bool split, hipStream_t s) {
