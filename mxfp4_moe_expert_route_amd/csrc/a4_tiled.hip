@@ -530,7 +530,7 @@ struct Tiled {
 #pragma unroll
               for (int c = 0; c < 3; ++c)
                 __builtin_amdgcn_raw_buffer_store_b32(
-                    __builtin_bit_cast(uint32_t, v[c]), ro,
+                    __float_as_uint(v[c]), ro,
                     live && col + 4 > p.N && col + c < p.N ? at + 4 * c : kDead, 0, 0);
             }
           } else {
