@@ -37,14 +37,15 @@ constexpr int kOneB = 512;                     // blocks that fill the CUs by th
 
 bool one_launch(int B, int V) { return V <= kOneT * kOwn || B >= kOneB; }
 
-// Parts per row where two launches are taken: about eight waves a CU, at
-// least 512 tokens a wave.
+// Parts per row where two launches are taken: about sixteen waves a CU, at
+// least 512 tokens a wave, and no more in a part than the draw takes at once.
 int parts_of(int B, int V) {
-  int n = 2048 / B;
-  const int most = (V + 511) / 512;
+  int n = 4096 / B;
+  const int most = (V + 511) / 512, least = (V + kDrawT * kOwn - 1) / (kDrawT * kOwn);
   n = n < most ? n : most;
-  n = n < kMaxParts ? n : kMaxParts;
-  return n < 4 ? 4 : n / 4 * 4;                // whole summing workgroups
+  n = n > least ? n : least;
+  n = (n + 3) / 4 * 4;                         // whole summing workgroups
+  return n < kMaxParts ? n : kMaxParts;
 }
 
 // Elements per part: whole 16-byte vectors of either type.
@@ -98,11 +99,35 @@ __device__ __forceinline__ void load(const uint16_t* p, int i, float (&v)[W]) {
   }
 }
 
+// The kOwn values from element i on; those from `end` on are 0.  vec: the row
+// is aligned and `end` a multiple of the vector.
+template <class T>
+__device__ __forceinline__ void load_run(const T* p, int i, int end, bool vec, float (&v)[kOwn]) {
+  constexpr int kW = 16 / int(sizeof(T));
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) v[k] = 0.f;
+  if (vec) {
+#pragma unroll
+    for (int h = 0; h < kOwn; h += kW) {
+      if (i + h < end) {
+        float x[kW];
+        load<kW>(p, i + h, x);
+#pragma unroll
+        for (int k = 0; k < kW; ++k) v[h + k] = x[k];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k)
+      if (i + k < end) v[k] = value(p, i + k);
+  }
+}
+
 // One wave's sum of the weights of tokens v0 .. v1 - 1; q may be NULL (0).
 // Loads of a round are issued together: a part's time is their latency.
 template <int W, class T>
 __device__ __forceinline__ double part_sum(const T* p, const T* q, int v0, int v1) {
-  constexpr int kU = W == 1 ? 8 : 3;
+  constexpr int kU = W == 1 ? 8 : 5;
   double s = 0.0;
   for (int base = v0; base < v1; base += kWave * W * kU) {
     float pv[kU][W], qv[kU][W];
@@ -190,7 +215,7 @@ __device__ __forceinline__ double block_prefix(double v, double* tot) {
 // The first thread for which `hit`, failing that the last for which `pos`
 // (a goal rounded onto the total), failing that -1.
 template <int NT>
-__device__ __forceinline__ int claim(bool hit, bool pos, unsigned long long* m) {
+__device__ __forceinline__ int claim(bool hit, bool pos, unsigned long long* m, bool* is_hit = nullptr) {
   constexpr int kW = NT / kWave;
   const unsigned long long h = __ballot(hit), p = __ballot(pos);
   __syncthreads();
@@ -203,6 +228,7 @@ __device__ __forceinline__ int claim(bool hit, bool pos, unsigned long long* m) 
 #pragma unroll
   for (int w = kW - 1; w >= 0; --w)
     if (m[w]) c = w * kWave + __ffsll((long long)m[w]) - 1;
+  if (is_hit) *is_hit = c >= 0;
   if (c >= 0) return c;
 #pragma unroll
   for (int w = 0; w < kW; ++w)
@@ -245,28 +271,39 @@ __device__ __forceinline__ int draw(const T* p, const T* q, int V, int parts, in
     const int part = claim<NT>(own > 0.0 && goal < incl, own > 0.0, s.mask);
     if (tid == part) s.base = incl - own;
     __syncthreads();
-    const double base = s.base;
-    // thread t owns a run of `each` tokens, so thread order is token order
-    const int v0 = min(part * span, V), v1 = min(v0 + span, V);
-    const int each = (v1 - v0 + NT - 1) / NT;
-    const int a0 = min(v0 + tid * each, v1), a1 = min(a0 + each, v1);
-    double run = 0.0;
-    for (int v = a0; v < a1; ++v) run += weight(value(p, v), q ? value(q, v) : 0.f);
-    const double end = base + block_prefix<NT>(run, s.tot);
-    const int c = claim<NT>(run > 0.0 && goal < end, run > 0.0, s.mask);
+    // NT kOwn of the part's tokens at a time; a thread owns a run of kOwn, so
+    // thread order is token order
+    double base = s.base;
+    const int v1 = min((part + 1) * span, V);
     int found = -1;
-    if (tid == c) {
-      double at = end - run;
-      for (int v = a0; v < a1; ++v) {
-        const double x = weight(value(p, v), q ? value(q, v) : 0.f);
-        if (x > 0.0) {
-          found = v;
-          at += x;
-          if (at > goal) break;
+    for (int v0 = min(part * span, V); v0 < v1; v0 += NT * kOwn) {
+      const int a0 = v0 + tid * kOwn;
+      float pv[kOwn], qv[kOwn];
+      load_run(p, a0, v1, vec, pv);
+      load_run(q, a0, q ? v1 : 0, vec, qv);
+      double run = 0.0;
+#pragma unroll
+      for (int k = 0; k < kOwn; ++k) run += weight(pv[k], qv[k]);
+      const double end = base + block_prefix<NT>(run, s.tot);
+      bool hit;
+      const int c = claim<NT>(run > 0.0 && goal < end, run > 0.0, s.mask, &hit);
+      if (c >= 0) found = -1;                  // a later token than any before
+      if (tid == c) {
+        double at = end - run;
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) {
+          const double x = weight(pv[k], qv[k]);
+          if (x > 0.0 && (found < 0 || !(at > goal))) {
+            found = a0 + k;
+            at += x;
+          }
         }
       }
+      if (hit) break;
+#pragma unroll
+      for (int w = 0; w < NT / kWave; ++w) base += s.tot[w];
     }
-    return found;                              // thread c's alone
+    return found;                              // one thread's alone
   }
 }
 
@@ -332,7 +369,7 @@ template <int NT, class T>
 __global__ __launch_bounds__(NT) void k_vp_own(
     const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
     const int32_t* __restrict__ draft_len, const float* __restrict__ uniforms, int L, int V,
-    int each, int32_t* __restrict__ accept_len, int32_t* __restrict__ next_token) {
+    int each, bool vec, int32_t* __restrict__ accept_len, int32_t* __restrict__ next_token) {
   __shared__ double tot[NT / kWave];
   __shared__ unsigned long long mask[2 * (NT / kWave)];
   const int b = blockIdx.x, tid = threadIdx.x;
@@ -341,25 +378,16 @@ __global__ __launch_bounds__(NT) void k_vp_own(
   const int n = blk.accepted();
   const T* p = blk.p(n);
   const T* q = blk.q(n);
-  const int a0 = min(tid * each, V), own = min(each, V - a0);
+  const int a0 = min(tid * each, V), a1 = min(a0 + each, V);
   float pv[kOwn], qv[kOwn];
-#pragma unroll
-  for (int k = 0; k < kOwn; ++k) {
-    pv[k] = qv[k] = 0.f;
-    if (k < own) {
-      pv[k] = value(p, a0 + k);
-      if (q) qv[k] = value(q, a0 + k);
-    }
-  }
+  load_run(p, a0, a1, vec, pv);
+  load_run(q, a0, q ? a1 : 0, vec, qv);
   if (tid == 0) accept_len[b] = n;
   bool residual = q != nullptr;
   for (;;) {
-    double w[kOwn], run = 0.0;
+    double run = 0.0;
 #pragma unroll
-    for (int k = 0; k < kOwn; ++k) {
-      w[k] = weight(pv[k], residual ? qv[k] : 0.f);
-      run += w[k];
-    }
+    for (int k = 0; k < kOwn; ++k) run += weight(pv[k], residual ? qv[k] : 0.f);
     const double incl = block_prefix<NT>(run, tot);
     double total = 0.0;
 #pragma unroll
@@ -379,9 +407,10 @@ __global__ __launch_bounds__(NT) void k_vp_own(
       double at = incl - run;
 #pragma unroll
       for (int k = 0; k < kOwn; ++k) {
-        if (w[k] > 0.0 && (found < 0 || !(at > goal))) {
+        const double x = weight(pv[k], residual ? qv[k] : 0.f);
+        if (x > 0.0 && (found < 0 || !(at > goal))) {
           found = a0 + k;
-          at += w[k];
+          at += x;
         }
       }
       next_token[b] = found;
@@ -398,15 +427,13 @@ hipError_t launch_typed(const void* target, const void* draft, const int32_t* to
   const T* q = static_cast<const T*>(draft);
   const bool vec = V % (16 / int(sizeof(T))) == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 &&
                    reinterpret_cast<uintptr_t>(q) % 16 == 0;
-  if (V <= kSplitT * kOwn) {
-    k_vp_own<kSplitT, T><<<unsigned(B), kSplitT, 0, s>>>(p, q, tokens, draft_len, uniforms, L, V,
-                                                         (V + kSplitT - 1) / kSplitT, accept_len,
-                                                         next_token);
-    return hipGetLastError();
-  }
   if (V <= kOneT * kOwn) {
-    k_vp_own<kOneT, T><<<unsigned(B), kOneT, 0, s>>>(p, q, tokens, draft_len, uniforms, L, V,
-                                                     (V + kOneT - 1) / kOneT, accept_len, next_token);
+    // whole vectors a thread, or as few tokens as there are threads for
+    const bool few = V <= kSplitT * kOwn;
+    const int nt = few ? kSplitT : kOneT;
+    (few ? k_vp_own<kSplitT, T> : k_vp_own<kOneT, T>)<<<unsigned(B), unsigned(nt), 0, s>>>(
+        p, q, tokens, draft_len, uniforms, L, V, vec ? kOwn : (V + nt - 1) / nt, vec, accept_len,
+        next_token);
     return hipGetLastError();
   }
   if (one_launch(B, V)) {
