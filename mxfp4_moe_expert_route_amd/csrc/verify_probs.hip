@@ -16,13 +16,15 @@
 //
 // Of the (L + 1) V probabilities of a block only the drafted tokens' entries
 // and the two rows at position n are read.  Up to 8192 tokens a workgroup per
-// block does it all, with its threads' weights in registers.  Beyond that a row
-// is cut into parts, one wave's sum each; the draw finds the part that holds it
-// and reads that one again.  A batch that fills the CUs by itself takes one
-// launch for that, a workgroup per block; a smaller one takes two, since fp64
-// sums over 152064 tokens keep one CU busy for about 16 us: the parts' sums by
-// workgroups that each find n themselves (2 L loads, cheaper than a launch),
-// then the draw.
+// block does it all, with its threads' weights in registers (64 blocks of 2048
+// tokens 4.0 us, 3 of 8192 6.7).  Beyond that two launches: the sums of a row's
+// parts, a wave each, by workgroups that each find n themselves (2 L loads,
+// cheaper than a launch); then the draw, a workgroup per block, which finds the
+// part that holds it and reads that one again, into registers.  One block of
+// 152064 tokens takes 8.4 us and 64 of them in bf16 16.5, latency of the two
+// launches' dependent loads for the most part; 1024 take 135, 4.6 TB/s, as fast
+// as a large copy.  (A workgroup per block throughout takes over 16 us for one
+// block and 150 for 1024.)
 #include "a4.hpp"
 
 namespace mxm {
@@ -33,9 +35,9 @@ constexpr int kDrawT = 512;
 constexpr int kOneT = 1024;                    // threads where one workgroup does it all
 constexpr int kMaxParts = 256;
 constexpr int kOwn = 8;                        // weights a thread holds in registers
-constexpr int kOneB = 512;                     // blocks that fill the CUs by themselves
 
-bool one_launch(int B, int V) { return V <= kOneT * kOwn || B >= kOneB; }
+// one launch, no workspace
+bool is_small(int V) { return V <= kOneT * kOwn; }
 
 // Parts per row where two launches are taken: about sixteen waves a CU, at
 // least 512 tokens a wave, and no more in a part than the draw takes at once.
@@ -341,27 +343,6 @@ __global__ __launch_bounds__(kDrawT) void k_vp_draw(
   if (t >= 0 || (!any && threadIdx.x == 0)) next_token[b] = t;
 }
 
-// One workgroup per block: its waves' parts are the row's.
-template <class T>
-__global__ __launch_bounds__(kOneT) void k_vp_one(
-    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
-    const int32_t* __restrict__ draft_len, const float* __restrict__ uniforms, int L, int V,
-    int span, bool vec, int32_t* __restrict__ accept_len, int32_t* __restrict__ next_token) {
-  constexpr int kParts = kOneT / kWave;
-  __shared__ DrawLds<kOneT> s;
-  const int b = blockIdx.x, part = threadIdx.x / kWave;
-  const Block<T> blk(target, draft, tokens, draft_len, uniforms, b, L, V);
-  const int n = blk.accepted();
-  const double sum =
-      part_sum(blk.p(n), blk.q(n), min(part * span, V), min((part + 1) * span, V), vec);
-  if (lane_id() == 0) s.sum[part] = sum;
-  __syncthreads();
-  const int t = draw<kOneT>(blk.p(n), blk.q(n), V, kParts, span, blk.u[L], vec, s);
-  const bool any = __syncthreads_or(t >= 0);
-  if (t >= 0 || (!any && threadIdx.x == 0)) next_token[b] = t;
-  if (threadIdx.x == 0) accept_len[b] = n;
-}
-
 // One workgroup per block and at most kOwn tokens per thread: thread t owns a
 // run of them, so thread order is token order and one prefix sum finds the
 // draw.
@@ -427,18 +408,13 @@ hipError_t launch_typed(const void* target, const void* draft, const int32_t* to
   const T* q = static_cast<const T*>(draft);
   const bool vec = V % (16 / int(sizeof(T))) == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 &&
                    reinterpret_cast<uintptr_t>(q) % 16 == 0;
-  if (V <= kOneT * kOwn) {
+  if (is_small(V)) {
     // whole vectors a thread, or as few tokens as there are threads for
     const bool few = V <= kSplitT * kOwn;
     const int nt = few ? kSplitT : kOneT;
     (few ? k_vp_own<kSplitT, T> : k_vp_own<kOneT, T>)<<<unsigned(B), unsigned(nt), 0, s>>>(
         p, q, tokens, draft_len, uniforms, L, V, vec ? kOwn : (V + nt - 1) / nt, vec, accept_len,
         next_token);
-    return hipGetLastError();
-  }
-  if (one_launch(B, V)) {
-    k_vp_one<T><<<unsigned(B), kOneT, 0, s>>>(p, q, tokens, draft_len, uniforms, L, V,
-                                              span_of(V, kOneT / kWave), vec, accept_len, next_token);
     return hipGetLastError();
   }
   const int parts = parts_of(B, V), span = span_of(V, parts);
@@ -455,7 +431,7 @@ hipError_t launch_typed(const void* target, const void* draft, const int32_t* to
 
 // the parts' sums, where two launches are taken
 size_t verify_probs_workspace_bytes(int B, int V) {
-  return one_launch(B, V) ? 0 : size_t(B) * parts_of(B, V) * sizeof(double);
+  return is_small(V) ? 0 : size_t(B) * parts_of(B, V) * sizeof(double);
 }
 
 hipError_t launch_verify_probs(const void* target, const void* draft, bool bf16,
