@@ -67,8 +67,8 @@ hipError_t launch_direct(Kind kind, Out out, const Problem& p, int ms, hipStream
 hipError_t launch_direct_gemm(Out out, const Problem& p, int cf, int ms, hipStream_t s);
 // Persistent, through LDS.  Grouped tiles are 32 ms rows tall, ms 1, 2 or 3
 // (split: experts with more rows in a launch of their own, with taller tiles);
-// the product's are 64 as columns x 32 ms rows: (4, 6), (2, 6), (2, 3), (2, 1)
-// or (1, 1).
+// the product's are 64 as columns x 32 ms rows: (4, 6), (2, 6), (2, 4), (2, 2)
+// or (2, 1).
 bool tiled_supported(Kind kind, const Problem& p);
 hipError_t launch_tiled(Kind kind, Out out, const Problem& p, int ms, bool split, hipStream_t s);
 hipError_t launch_tiled_gemm(Out out, const Problem& p, int as, int ms, hipStream_t s);

@@ -36,19 +36,25 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Which kernel and tile a product takes: the one whose time, estimated from
 // sizes alone, is least.  A direct unit costs the loads of its fragments, 70
-// ns each per 256 of K and CU; a tiled item the stages of its tile (fits of
-// measured times to about 20%).  In us, 8 x 4096 x 6144: direct (1, 1) 4.8,
-// tiled 64 x 32 11; 333 x 1001 x 2080: direct (2, 4) 6.6, tiled 64 x 32 7.0,
-// 256 x 192 27; 512 x 6144 x 2048: tiled 128 x 192 14, 256 x 192 21, 64 x 32
-// 24; 8192 x 4096 x 6144: 256 x 192 145, 128 x 192 170, 128 x 96 207.
+// ns each per 256 of K and CU.  A tiled item costs the stages of its tile and
+// its epilogue; a stage takes longer the more CUs are busy (they share L2 and
+// power), so a last, partial round goes faster.  The constants are fits of
+// measured times, to about 15%.  In us, by tile 256 x 192, 128 x 192, 128 x 128,
+// 128 x 64, 128 x 32: 512 x 6144 x 2048 20.9, 14.0, 11.9, 13.8, 16.2; 333 x 4096
+// x 6144 35.8, 23.4, 19.1, 15.7, 26.3; 260 x 2049 x 2048 18.3, 11.8, 9.8, 8.3,
+// 7.5; 4096 x 4096 x 4096 58, 53, 55, 67, 113; 8192 x 4096 x 6144 131, 170 by the
+// first two.  Direct: 8 x 4096 x 6144 4.8 (11 by 128 x 32).
 hipError_t product(mxm::a4::Out out, const Problem& p, hipStream_t s) {
   struct Tile {
     int a, ms;
-    double stage, item;                  // tiled: us per stage of 256 of K, per item
+    double idle, busy, item;             // tiled: us per stage of 256 of K, per item
   };
-  constexpr Tile kDirect[] = {{1, 1, 0, 0}, {1, 2, 0, 0}, {2, 2, 0, 0}, {2, 4, 0, 0}};
-  constexpr Tile kTiled[] = {
-      {4, 6, 1.8, 6.0}, {2, 6, 1.15, 3.5}, {2, 3, 0.75, 2.2}, {2, 1, 0.45, 1.2}, {1, 1, 0.33, 1.0}};
+  constexpr Tile kDirect[] = {{1, 1}, {1, 2}, {2, 2}, {2, 4}};
+  constexpr Tile kTiled[] = {{4, 6, 0.93, 1.4, 8.0},
+                             {2, 6, 0.60, 0.9, 3.2},
+                             {2, 4, 0.42, 0.64, 2.7},
+                             {2, 2, 0.40, 0.40, 1.6},
+                             {2, 1, 0.35, 0.35, 1.0}};
   constexpr int kCus = 256;
   const double chunks = double(ceil_div(p.K, 256));
   double best = 1e30;
@@ -62,7 +68,9 @@ hipError_t product(mxm::a4::Out out, const Problem& p, hipStream_t s) {
   if (mxm::a4::tiled_supported(mxm::a4::kGemm, p)) {
     for (const Tile& c : kTiled) {
       const int64_t items = ceil_div(p.N, 64 * c.a) * ceil_div(p.M, 32 * c.ms);
-      const double us = 3.0 + double(ceil_div(items, kCus)) * (chunks * c.stage + c.item);
+      const double last = double(items % kCus) / kCus;
+      const double us = 4.3 + double(ceil_div(items, kCus)) * c.item + double(items / kCus) * chunks * c.busy +
+                        (last > 0 ? chunks * (c.idle + last * (c.busy - c.idle)) : 0.0);
       if (us < best) best = us, t = &c, tiled = true;
     }
   }

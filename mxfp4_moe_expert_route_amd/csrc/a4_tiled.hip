@@ -779,9 +779,9 @@ hipError_t launch_grouped(const Problem& p, int ms, bool split, hipStream_t s) {
 template <Out OUT>
 hipError_t launch_gemm(const Problem& p, int as, int ms, hipStream_t s) {
   if (as == 4) return launch_k<kGemm, OUT, 4, 6>(p, s);
-  if (as == 1) return launch_k<kGemm, OUT, 1, 1>(p, s);
   if (ms == 6) return launch_k<kGemm, OUT, 2, 6>(p, s);
-  if (ms == 3) return launch_k<kGemm, OUT, 2, 3>(p, s);
+  if (ms == 4) return launch_k<kGemm, OUT, 2, 4>(p, s);
+  if (ms == 2) return launch_k<kGemm, OUT, 2, 2>(p, s);
   return launch_k<kGemm, OUT, 2, 1>(p, s);
 }
 

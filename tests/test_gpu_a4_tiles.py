@@ -46,11 +46,11 @@ def exact(a, b, lo_a, lo_b):
     return a @ b.T
 
 
-# columns and rows of a tile: 64 x 32 (at few rows and many columns), 128 x 32,
-# 128 x 96, 128 x 192, 256 x 192
+# tiles of 128 columns and 32, 64, 128 and 192 rows, and of 256 x 192
 TILES = [(7, 13137, 2048), (7, 13137, 1632), (260, 2049, 2048), (260, 2049, 1184), (700, 2701, 1024),
          (700, 2702, 544), (1500, 2049, 512), (1500, 2051, 544), (7390, 771, 512), (4537, 1337, 544),
-         (4537, 1337, 2048), (4540, 1340, 2080)]
+         (4537, 1337, 2048), (4540, 1340, 2080), (260, 2049, 2080), (4537, 2339, 2048), (4537, 2341, 2080),
+         (8190, 3333, 2048), (8190, 3335, 2080)]
 
 
 @pytest.mark.parametrize("M,N,K", TILES)
@@ -71,7 +71,8 @@ def test_gemm_tiles(mm, M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(7, 13137, 1632), (260, 2049, 1184), (260, 2049, 2048), (700, 2702, 544),
-                                   (1500, 2051, 544), (4537, 1337, 544), (4537, 1337, 2048)])
+                                   (1500, 2051, 544), (4537, 1337, 544), (4537, 1337, 2048),
+                                   (260, 2049, 2080), (4537, 2341, 2080), (8190, 3335, 2080)])
 def test_gemm_tiles_nan_scales(mm, M, N, K):
     """A NaN block makes its own row (column) NaN and no other, first and last
     blocks of neighbouring rows among them."""
