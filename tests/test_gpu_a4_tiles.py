@@ -127,12 +127,14 @@ def routing(gen, T, E, k, skew):
     return order, offsets, n
 
 
-# rows of a tile: 32, 64, 96; 32 and taller experts apart (two sizes); 64, 96
+# rows of a tile: 32, 64, 96; 32 and taller experts apart (two sizes); 64, 96;
+# and more items than a workgroup lays out at a time
 GATE_UP = [(1200, 1024, 544, 3, 1), (1200, 1056, 544, 3, 1), (1200, 1024, 1056, 3, 1),
            (1200, 1056, 1056, 3, 1), (1200, 1024, 1056, 3, 2), (1200, 1056, 1056, 3, 2),
            (200, 2048, 2080, 64, 2), (200, 2080, 2080, 64, 2), (700, 2048, 2080, 64, 4),
            (700, 2080, 2080, 64, 4), (1200, 1024, 2080, 9, 8), (1200, 1056, 2080, 9, 8),
-           (1200, 2048, 2080, 8, 4), (1200, 2080, 2080, 8, 4)]
+           (1200, 2048, 2080, 8, 4), (1200, 2080, 2080, 8, 4), (2000, 1024, 1056, 1024, 4),
+           (2000, 1056, 1056, 1024, 4)]
 
 
 @pytest.mark.parametrize("T,H,I,E,k", GATE_UP)
@@ -145,7 +147,7 @@ def test_gate_up_tiles(mm, T, H, I, E, k):
     h = torch.full((T * k, I), -7.0, dtype=torch.bfloat16, device=DEV)
     mm.moe_mxfp4_a4_gate_up_swiglu(*x, pairs, offsets, k, *w, h=h)
     x64, off = f64(*x), offsets.tolist()
-    for e in range(E):
+    for e in range(0, E, 1 if E < 100 else 13):
         if off[e] == off[e + 1]:
             continue
         rows = slice(off[e], off[e + 1])
@@ -154,7 +156,7 @@ def test_gate_up_tiles(mm, T, H, I, E, k):
         want = g * torch.sigmoid(g) * u
         tol = (2.0 ** -8 + 2.0 ** -21 * (2 + g.abs())) * want.abs() + 2.0 ** -126
         assert bool(((h[rows].double() - want).abs() <= tol).all()), e
-    assert bool((h[n:] == -7).all())
+    assert bool((h[n:] == -7).all()) and not bool((h[:n] == -7).all(1).any())
     hc = torch.full((T * k, I // 2), 0x5a, dtype=torch.uint8, device=DEV)
     hs = torch.full((T * k, I // 32), 0x5a, dtype=torch.uint8, device=DEV)
     mm.moe_mxfp4_a4_gate_up_swiglu_pack(*x, pairs, offsets, k, *w, h_codes=hc, h_scales=hs)
@@ -165,7 +167,8 @@ def test_gate_up_tiles(mm, T, H, I, E, k):
 
 DOWN = [(700, 1056, 512, 3, 1), (700, 1056, 1056, 3, 1), (1200, 1056, 512, 3, 2), (1200, 1056, 1056, 3, 2),
         (1200, 2080, 512, 3, 2), (1200, 2080, 1056, 3, 2), (1200, 2080, 2048, 9, 8), (1200, 2080, 2080, 17, 8),
-        (300, 8192, 2048, 64, 4), (300, 8192, 2080, 64, 4), (700, 8192, 2048, 64, 4), (700, 8192, 2080, 64, 4)]
+        (300, 8192, 2048, 64, 4), (300, 8192, 2080, 64, 4), (700, 8192, 2048, 64, 4), (700, 8192, 2080, 64, 4),
+        (2000, 2336, 512, 1024, 4), (2000, 2336, 1056, 1024, 4)]
 
 
 @pytest.mark.parametrize("T,H,I,E,k", DOWN)
@@ -178,9 +181,9 @@ def test_down_tiles(mm, T, H, I, E, k):
     y = torch.full((T * k, H), -7.0, device=DEV)
     mm.moe_mxfp4_a4_down(*h, offsets, k, *w, y=y)
     off = offsets.tolist()
-    for e in range(E):
+    for e in range(0, E, 1 if E < 100 else 13):
         rows = slice(off[e], off[e + 1])
         if off[e] < off[e + 1]:
             want = exact(f64(h[0][rows], h[1][rows]), f64(w[0][e], w[1][e]), lo, lo)
             assert torch.equal(y[rows].double(), want), e
-    assert bool((y[n:] == -7).all())
+    assert bool((y[n:] == -7).all()) and not bool((y[:n] == -7).all(1).any())
