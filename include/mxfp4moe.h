@@ -365,8 +365,8 @@ int moe_mxfp4_layer_noalloc(const uint16_t* x_bf16, const float* logits, int T, 
  * (RNE).  Every scale byte is taken as mxfp4_unpack takes it: 0 is 2^-127 and
  * 255 makes the rows (columns) it belongs to NaN; where the products'
  * magnitudes sum past fp32's range the result may be Inf or NaN.
- * Deterministic.  K a
- * multiple of 32 from 32 to 2^20; any M and N, 0 being a no-op.
+ * Deterministic.  K a multiple of 32 from 32 to 2^20; M and N up to 2^30, 0
+ * being a no-op.
  * The pages store weights in MXFP4 (model card, §2 "FP4 Quantization") and
  * keep activations in higher precision; MXFP4 activations are an addition.
  */
@@ -422,8 +422,8 @@ int moe_mxfp4_a4_layer(const uint16_t* x_bf16, const float* logits, int T, int H
                        uint8_t* h_codes, uint8_t* h_scales, float* y, float* out,
                        void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace dflash_verify_probs needs: 0 where one launch does it all (small
- * vocabularies, large batches) and for invalid sizes. */
+/* Workspace dflash_verify_probs needs: 0 where one launch does it all
+ * (vocabularies of up to 8192) and for invalid sizes. */
 size_t dflash_verify_probs_workspace_bytes(int B, int L, int V);
 
 /*

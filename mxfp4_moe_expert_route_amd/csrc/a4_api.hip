@@ -17,6 +17,7 @@ constexpr int kMaxK = 32;
 constexpr int kMaxH = 16384;
 constexpr int kMaxI = 8192;
 constexpr int kMaxGemmK = 1 << 20;
+constexpr int kMaxGemmMN = 1 << 30;      // rows and columns are counted in 31 bits, past the last tile too
 constexpr int kMaxVerifyL = 32;          // one lane of a wave per block position
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -43,7 +44,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // 128 x 64, 128 x 32: 512 x 6144 x 2048 20.9, 14.0, 11.9, 13.8, 16.2; 333 x 4096
 // x 6144 35.8, 23.4, 19.1, 15.7, 26.3; 260 x 2049 x 2048 18.3, 11.8, 9.8, 8.3,
 // 7.5; 4096 x 4096 x 4096 58, 53, 55, 67, 113; 8192 x 4096 x 6144 131, 170 by the
-// first two.  Direct: 8 x 4096 x 6144 4.8 (11 by 128 x 32).
+// first two.  Direct: 8 x 4096 x 6144 5 (11 by 128 x 32).
 hipError_t product(mxm::a4::Out out, const Problem& p, hipStream_t s) {
   struct Tile {
     int a, ms;
@@ -127,7 +128,8 @@ extern "C" {
 int mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
                const uint8_t* b_scales, int M, int N, int K, void* c, int c_dtype, void* stream) {
   if (c_dtype != MXM_F32 && c_dtype != MXM_BF16) return MXM_ERR_DTYPE;
-  if (M < 0 || N < 0 || K < 32 || K % 32 || K > kMaxGemmK) return MXM_ERR_SHAPE;
+  if (M < 0 || N < 0 || M > kMaxGemmMN || N > kMaxGemmMN) return MXM_ERR_SHAPE;
+  if (K < 32 || K % 32 || K > kMaxGemmK) return MXM_ERR_SHAPE;
   if (M == 0 || N == 0) return MXM_OK;
   if (!a_codes || !a_scales || !b_codes || !b_scales || !c) return MXM_ERR_NULL;
   if (!aligned(a_codes, 16) || !aligned(b_codes, 16) || !aligned(c, c_dtype == MXM_F32 ? 4 : 2))

@@ -8,7 +8,7 @@
 // sums meet in LDS, added in wave order, so results do not depend on timing:
 // splitting K rather than the columns keeps every byte of a unit in flight at
 // once, and with few rows the cost is the latency of the weight bytes, not
-// their number (8 x 4096 x 6144: 4.8 us for 12.6 MB).  Where K is a few chunks,
+// their number (8 x 4096 x 6144: 5 us for 12.6 MB).  Where K is a few chunks,
 // each wave has a unit to itself.
 #include "a4.hpp"
 #include "mx_pack.hpp"

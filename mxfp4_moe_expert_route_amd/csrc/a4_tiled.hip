@@ -1,37 +1,48 @@
 // Contractions of two MXFP4 factors through LDS: a persistent kernel on the
 // scaled matrix instructions.
 //
-// Work items: (expert, n-tile of 64 AS weight rows, m-tile of at most 192
+// Work items: (expert, n-tile of 64 AS weight rows, m-tile of at most 32 MS
 // rows), expert by expert; within one, blocks of eight m-tiles run through
 // the n-tiles.  The list is cut into eight contiguous ranges, one per XCD
 // (workgroup b runs on XCD b % 8), whose workgroups, one per CU, take its
 // items in rounds, ascending and descending in turn.  Neighbouring items run
 // side by side and share weight or activation rows in that XCD's L2; an
-// expert of up to 192 rows has its weights read once.
+// expert whose rows fit one tile has its weights read once.
 //
 // The loads are one endless stream: a workgroup's items are laid out in a
-// table first, and the loaders run up to three stages ahead of the matrix
-// instructions, across item boundaries, so a new item starts with its first
-// stages already in LDS.
+// table first, and the loaders run two stages (weights three to five) ahead of
+// the matrix instructions, across item boundaries, so a new item starts with
+// its first stages already in LDS.
 //
 // A stage is 256 of K: one 128-byte line of codes per row, loaded by eight
 // adjacent lanes (whole lines read 15% faster from HBM than half lines: 7.1
 // against 6.1 TB/s in a copy of the weight stream alone).  16-byte piece p of
-// row r lies at slot p ^ (r % 8) of the row's 128 bytes, which reads without
-// bank conflicts at the full rate (measured: 256 bytes per clock, as linear
-// reads; r % 4 or r / 2 in its place 160).  Weights go through a ring of
-// kRingW stages, activations through two, scale bytes 16 at a time (two
-// stages' worth) through two buffers.
+// row r lies at slot p ^ (r % 8) of the row's 128 bytes, which reads as fast as
+// linear addresses do (p ^ (r % 4) and p ^ (r / 2 % 8) at 0.6 of that).  Weights
+// go through a ring of kRingW stages, activations through two.  Scales are
+// loaded 32 bytes of a row at a time (four stages' worth) into registers and
+// written to one LDS buffer a stage later, transposed, so that a lane finds its
+// four steps' bytes in one dword.
 //
 // Eight waves, 4 x 2, two per SIMD: wave (wn, wm) computes AS 16-row weight
 // subtiles x the 16-row subtiles wm, wm + 2, ... of the tile's rows.  A stage
 // is two steps of 128; the operands of a step are read from LDS while the
-// step before it multiplies.  One barrier per stage, between its steps: past
-// it every wave has read all of stage t (its slots are free) and stage t + 1
-// has landed.
+// step before it multiplies, and the stage's loads are spread over its
+// products.  One barrier per stage, between its steps: past it every wave has
+// read all of stage t (its slots are free) and stage t + 1 has landed.
 //
-// Matrix rows past a tile's end are not loaded and not stored; blocks past
-// the end of K load as zero codes under scale 1.
+// Matrix rows past a tile's end are not loaded and not stored; pieces past the
+// end of K load as zero codes.  A row's blocks past its end have scales of that
+// row's own, so a NaN among them is one that the row's result holds anyway.
+//
+// What bounds it.  8192 x 4096 x 6144 takes 127-137 us, 3.0-3.2 PFLOP/s: the
+// products alone, from registers, reach 5.8-6.5 PFLOP/s, and with HBM and LDS
+// busy beside them the clock falls to 1.7-1.9 GHz; a tenth of the time goes to
+// 2.7 rounds of tiles being three.  The page-shaped gate/up (384 experts, 6144 x
+// 2 2048) takes 1.31 ms at 8192 tokens (1.10 at a large copy's rate) and 135 us
+// at 8 (6.1 TB/s, of 7.1 that reads alone reach); down 0.88 ms at 8192 (0.86 at
+// a copy's rate) and 299 us at 64 (6.4 TB/s).  An activation ring of three
+// stages was no faster at any size.
 #include "a4.hpp"
 #include "mx_pack.hpp"
 

@@ -21,6 +21,8 @@ def test_gemm_argument_checks(lib):
     assert f(P, P, P, P, 4, 8, 0, P, 0, None) == -2
     assert f(P, P, P, P, 4, 8, (1 << 20) + 32, P, 0, None) == -2
     assert f(P, P, P, P, -1, 8, 64, P, 0, None) == -2
+    assert f(P, P, P, P, (1 << 30) + 1, 8, 32, P, 0, None) == -2
+    assert f(P, P, P, P, 8, (1 << 30) + 1, 32, P, 0, None) == -2
     assert f(P, P, P, P, 4, -8, 64, P, 0, None) == -2
     for i in range(4):
         a = [P] * 4
