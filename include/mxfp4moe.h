@@ -449,7 +449,7 @@ size_t dflash_verify_probs_workspace_bytes(int B, int L, int V);
  * entry there is no token: next_token is -1.  A drafted token outside [0, V)
  * is rejected.  Acceptance is decided exactly; sums are in fp64 in a fixed
  * order, so a draw may differ from exact arithmetic only within 2^-35 of a
- * boundary, relative to the sum.  1 <= L <= 32, 1 <= V <= 2^30, B <= 2^24.
+ * boundary, relative to the sum.  1 <= L <= 32, 1 <= V <= 2^30, B <= 2^20.
  * Elements need only their own alignment.
  */
 int dflash_verify_probs(const void* target_probs, const void* draft_probs, int dtype,

@@ -19,6 +19,7 @@ constexpr int kMaxI = 8192;
 constexpr int kMaxGemmK = 1 << 20;
 constexpr int kMaxGemmMN = 1 << 30;      // rows and columns are counted in 31 bits, past the last tile too
 constexpr int kMaxVerifyL = 32;          // one lane of a wave per block position
+constexpr int kMaxVerifyB = 1 << 20;     // a launch has fewer than 2^32 threads, 1024 a block
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -235,7 +236,7 @@ int dflash_verify_probs(const void* target_probs, const void* draft_probs, int d
                         void* stream) {
   if (dtype != MXM_F32 && dtype != MXM_BF16) return MXM_ERR_DTYPE;
   // parts of a block and a row's elements are counted in 31 bits
-  if (B < 0 || B > (1 << 24) || L < 1 || L > kMaxVerifyL || V < 1 || V > (1 << 30))
+  if (B < 0 || B > kMaxVerifyB || L < 1 || L > kMaxVerifyL || V < 1 || V > (1 << 30))
     return MXM_ERR_SHAPE;
   if (B == 0) return MXM_OK;
   const size_t need = dflash_verify_probs_workspace_bytes(B, L, V);

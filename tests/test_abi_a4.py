@@ -97,6 +97,7 @@ def test_verify_probs_argument_checks(lib):
     assert f(P, P, 0, P, None, P, 4, 33, V, P, P, P, ws, None) == -2
     assert f(P, P, 0, P, None, P, 4, 8, 0, P, P, P, ws, None) == -2
     assert f(P, P, 0, P, None, P, (1 << 24) + 1, 8, V, P, P, P, 1 << 40, None) == -2
+    assert f(P, P, 0, P, None, P, (1 << 20) + 1, 1, 3, P, P, P, 0, None) == -2
     assert f(P, P, 0, P, None, P, 4, 8, V, P, P, P, ws - 1, None) == -7
     assert f(P, None, 0, P, None, P, 4, 8, V, P, P, P, ws, None) == -1
     assert f(P, P, 0, P, None, P, 4, 8, V, P, P, None, ws, None) == -1

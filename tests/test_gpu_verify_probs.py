@@ -154,3 +154,29 @@ def test_captured_and_replayed(mm):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out[0], sets[i % 2][1][0]) and torch.equal(out[1], sets[i % 2][1][1]), i
+
+
+@pytest.mark.parametrize("V", [3, 2500])
+def test_largest_batch(mm, V):
+    """2^20 blocks, both one-launch forms.  Probabilities are multiples of 1/4
+    and uniforms of 2^-10, so every sum and comparison is exact."""
+    say("verify_probs, 2^20 blocks", V)
+    B = 1 << 20
+    g = torch.Generator(device=DEV).manual_seed(V)
+    p, q = (torch.randint(0, 5, (B, n, V), device=DEV, generator=g, dtype=torch.int8).to(torch.bfloat16) / 4
+            for n in (2, 1))
+    tokens = torch.randint(0, V, (B, 1), device=DEV, generator=g).int()
+    u = torch.randint(0, 1024, (B, 2), device=DEV, generator=g).float() / 1024
+    n, t = mm.dflash_verify_probs(p, q, tokens, u)
+    for b0 in range(0, B, 1 << 16):
+        rows = slice(b0, min(b0 + (1 << 16 if V < 100 else 2048), B))      # of the larger, part
+        pr, qr, d = p[rows].float(), q[rows, 0].float(), tokens[rows].long()
+        accept = u[rows, :1] * qr.gather(1, d) < pr[:, 0].gather(1, d)
+        rest = (pr[:, 0] - qr).clamp_min(0)
+        rest = torch.where(rest.sum(1, keepdim=True) > 0, rest, pr[:, 0])
+        w = torch.where(accept, pr[:, 1], rest)
+        cum = w.cumsum(1)
+        total = cum[:, -1:]
+        want = torch.where(total > 0, (cum <= u[rows, 1:] * total).sum(1, keepdim=True), -1)
+        assert torch.equal(n[rows], accept[:, 0].int())
+        assert torch.equal(t[rows], want[:, 0].int())
