@@ -87,7 +87,7 @@ hipError_t product(mxm::a4::Out out, const Problem& p, hipStream_t s) {
 // 1154 us at 512 tokens (11 rows an expert); 1372, 933, 1005, 1181 at 2048 (43);
 // 2085, 1483, 1211, 1256 at 4096 (85); 3921, 2217, 1678, 1390 at 8192 (171).
 // Routing is skewed as a rule, so the experts that outgrow the tile go to a
-// taller one in a launch of their own: Zipf-routed, 512 tokens take 525 us so
+// taller one in a launch of their own: Zipf-routed, 512 tokens take 544 us so
 // and 637 with 32-row tiles alone.  Where there is nothing for it that launch
 // costs about 4 us: small calls and batches with few rows an expert do without.
 hipError_t grouped(mxm::a4::Kind kind, mxm::a4::Out out, const Problem& p, hipStream_t s) {

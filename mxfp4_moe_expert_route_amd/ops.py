@@ -342,14 +342,21 @@ def moe_mxfp4_layer_noalloc(x, logits, k, w13_codes, w13_scales, w2_codes, w2_sc
 
 # ---- MXFP4 activations, and verification from probabilities ----------------
 
+_Tensor = torch.Tensor
+_functions = {}
+
+
 def _enqueue(name, device, *args):
     """Call the library on `device`'s current stream (whatever device is current)."""
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(lib(), name)
     i = device.index
     if i == torch._C._cuda_getDevice():
-        st = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(i))
+        st = f(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
         with torch.cuda.device(device):
-            st = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(i))
+            st = f(*args, torch._C._cuda_getCurrentRawStream(i))
     if st:
         check(st, name)
 
@@ -357,7 +364,7 @@ def _enqueue(name, device, *args):
 def _want(t, name, dtype, shape, device):
     """_need, quickly where it holds: a call makes five of these checks and
     lasts a few microseconds itself."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and
+    if not (type(t) is _Tensor and t.dtype is dtype and t.shape == shape and
             t.get_device() == device.index and t.is_contiguous()):
         _need(t, name, dtype, shape, device)
 
@@ -393,8 +400,8 @@ def mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, dtype=torch.float32, out=No
     _need_mx(a_codes, a_scales, "a", (M, K), dev)
     _need_mx(b_codes, b_scales, "b", (N, K), dev)
     out = _result(out, "out", dtype, (M, N), dev)
-    _enqueue("mxfp4_gemm", dev, _ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), M, N,
-             K, _ptr(out), BF16 if dtype == torch.bfloat16 else F32)
+    _enqueue("mxfp4_gemm", dev, a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(),
+             b_scales.data_ptr(), M, N, K, out.data_ptr(), BF16 if dtype == torch.bfloat16 else F32)
     return out
 
 
@@ -415,8 +422,9 @@ def moe_mxfp4_a4_gate_up_swiglu(x_codes, x_scales, sorted_pairs, offsets, k, w13
     T, H, I, E, dev = _a4_gate_up_shapes(x_codes, x_scales, sorted_pairs, offsets, k, w13_codes,
                                          w13_scales)
     h = _result(h, "h", torch.bfloat16, (T * k, I), dev)
-    _enqueue("moe_mxfp4_a4_gate_up_swiglu", dev, _ptr(x_codes), _ptr(x_scales), _ptr(sorted_pairs),
-             _ptr(offsets), T, H, I, E, k, _ptr(w13_codes), _ptr(w13_scales), _ptr(h), None, None)
+    _enqueue("moe_mxfp4_a4_gate_up_swiglu", dev, x_codes.data_ptr(), x_scales.data_ptr(),
+             sorted_pairs.data_ptr(), offsets.data_ptr(), T, H, I, E, k, w13_codes.data_ptr(),
+             w13_scales.data_ptr(), h.data_ptr(), None, None)
     return h
 
 
@@ -428,9 +436,9 @@ def moe_mxfp4_a4_gate_up_swiglu_pack(x_codes, x_scales, sorted_pairs, offsets, k
                                          w13_scales)
     h_codes = _result(h_codes, "h_codes", torch.uint8, (T * k, I // 2), dev)
     h_scales = _result(h_scales, "h_scales", torch.uint8, (T * k, I // 32), dev)
-    _enqueue("moe_mxfp4_a4_gate_up_swiglu", dev, _ptr(x_codes), _ptr(x_scales), _ptr(sorted_pairs),
-             _ptr(offsets), T, H, I, E, k, _ptr(w13_codes), _ptr(w13_scales), None, _ptr(h_codes),
-             _ptr(h_scales))
+    _enqueue("moe_mxfp4_a4_gate_up_swiglu", dev, x_codes.data_ptr(), x_scales.data_ptr(),
+             sorted_pairs.data_ptr(), offsets.data_ptr(), T, H, I, E, k, w13_codes.data_ptr(),
+             w13_scales.data_ptr(), None, h_codes.data_ptr(), h_scales.data_ptr())
     return h_codes, h_scales
 
 
@@ -445,8 +453,8 @@ def moe_mxfp4_a4_down(h_codes, h_scales, offsets, k, w2_codes, w2_scales, y=None
     _need_mx(w2_codes, w2_scales, "w2", (E, H, I), dev)
     _want(offsets, "offsets", torch.int32, (E + 1,), dev)
     y = _result(y, "y", torch.float32, (R, H), dev)
-    _enqueue("moe_mxfp4_a4_down", dev, _ptr(h_codes), _ptr(h_scales), _ptr(offsets), R // k, H, I,
-             E, k, _ptr(w2_codes), _ptr(w2_scales), _ptr(y))
+    _enqueue("moe_mxfp4_a4_down", dev, h_codes.data_ptr(), h_scales.data_ptr(), offsets.data_ptr(),
+             R // k, H, I, E, k, w2_codes.data_ptr(), w2_scales.data_ptr(), y.data_ptr())
     return y
 
 
@@ -523,9 +531,9 @@ def dflash_verify_probs(target_probs, draft_probs, draft_tokens, uniforms, draft
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     else:
         _need(workspace, "workspace", torch.uint8, None, dev)
-    _enqueue("dflash_verify_probs", dev, _ptr(target_probs), _ptr(draft_probs),
-             BF16 if dtype == torch.bfloat16 else F32, _ptr(draft_tokens), _ptr(draft_len),
-             _ptr(uniforms), B, L, V, _ptr(accept_len), _ptr(next_token), _ptr(workspace),
+    _enqueue("dflash_verify_probs", dev, target_probs.data_ptr(), draft_probs.data_ptr(),
+             BF16 if dtype == torch.bfloat16 else F32, draft_tokens.data_ptr(), _ptr(draft_len),
+             uniforms.data_ptr(), B, L, V, accept_len.data_ptr(), next_token.data_ptr(), _ptr(workspace),
              0 if workspace is None else workspace.numel())
     return accept_len, next_token
 
