@@ -341,9 +341,15 @@ struct Tiled {
   // Next stage of the activation stream: where it goes; a new item's rows; new
   // scales.  Past the stream's end the loads are dead: they move nothing, and
   // keep the count of loads the same in every stage.
+  //
+  // The scalar offset stays below a row's bytes.  A buffer load's range check
+  // compares the vector offset with the buffer's size less the scalar one,
+  // unsigned: past the end of a buffer of one row (K = 544: 272 bytes, the
+  // fourth stage at 384) that would wrap, and dead offsets be inside.  A stage
+  // past the row has dead pieces alone.
   __device__ __forceinline__ void next_x() {
     xdst = L::kX + (xt & 1) * L::kXSlot;
-    xso = 128 * xs;
+    xso = (WHOLE || 128 * xs < rowb) ? 128 * xs : 0;
     xtail = 0;
     ++xt;
     if (xi >= cnt) {
