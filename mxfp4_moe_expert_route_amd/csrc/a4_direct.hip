@@ -33,12 +33,16 @@ struct Frag {
   uint32_t s[2];         // and their scale bytes
 };
 
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+
 // Store at an address aligned to its elements alone (a row may start anywhere).
+// T is a vector type of the compiler: a class such as uint2 is not packed.
 template <class T>
 __device__ __forceinline__ void store_any(void* p, const T& v) {
   struct __attribute__((packed, aligned(2))) U {
     T v;
   };
+  static_assert(alignof(U) == 2, "the store may not claim more alignment than it has");
   static_cast<U*>(p)->v = v;
 }
 
@@ -221,7 +225,7 @@ __global__ __launch_bounds__(kThreads) void k_direct(Problem p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) b[i] = f32_to_bf16_rne(v[i]);
             if (n + 4 <= p.N) {
-              store_any(o, make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16)));
+              store_any(o, u32x2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)});
             } else {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
