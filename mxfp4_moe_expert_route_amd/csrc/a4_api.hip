@@ -20,6 +20,7 @@ constexpr int kMaxGemmK = 1 << 20;
 constexpr int kMaxGemmMN = 1 << 30;      // rows and columns are counted in 31 bits, past the last tile too
 constexpr int kMaxVerifyL = 32;          // one lane of a wave per block position
 constexpr int kMaxVerifyB = 1 << 20;     // a launch has fewer than 2^32 threads, 1024 a block
+constexpr int kMaxVerifyV = 1 << 30;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -32,6 +33,11 @@ int check_ffn_shape(int T, int H, int I, int E, int k) {
   if (int64_t(T) * k > INT32_MAX) return MXM_ERR_SHAPE;
   if (H < 32 || I < 32 || H % 32 || I % 32 || H > kMaxH || I > kMaxI) return MXM_ERR_SHAPE;
   return MXM_OK;
+}
+
+// parts of a block and a row's elements are counted in 31 bits
+bool verify_probs_shape(int B, int L, int V) {
+  return B >= 0 && B <= kMaxVerifyB && L >= 1 && L <= kMaxVerifyL && V >= 1 && V <= kMaxVerifyV;
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -225,7 +231,7 @@ int moe_mxfp4_a4_layer(const uint16_t* x_bf16, const float* logits, int T, int H
 }
 
 size_t dflash_verify_probs_workspace_bytes(int B, int L, int V) {
-  if (B < 1 || L < 1 || L > kMaxVerifyL || V < 1) return 0;
+  if (B == 0 || !verify_probs_shape(B, L, V)) return 0;
   return mxm::verify_probs_workspace_bytes(B, V);
 }
 
@@ -235,9 +241,7 @@ int dflash_verify_probs(const void* target_probs, const void* draft_probs, int d
                         int32_t* next_token, void* workspace, size_t workspace_bytes,
                         void* stream) {
   if (dtype != MXM_F32 && dtype != MXM_BF16) return MXM_ERR_DTYPE;
-  // parts of a block and a row's elements are counted in 31 bits
-  if (B < 0 || B > kMaxVerifyB || L < 1 || L > kMaxVerifyL || V < 1 || V > (1 << 30))
-    return MXM_ERR_SHAPE;
+  if (!verify_probs_shape(B, L, V)) return MXM_ERR_SHAPE;
   if (B == 0) return MXM_OK;
   const size_t need = dflash_verify_probs_workspace_bytes(B, L, V);
   if (workspace_bytes < need) return MXM_ERR_WORKSPACE;

@@ -125,3 +125,13 @@ def test_wrappers_refuse_host_tensors_and_wrong_ranks():
         mm.dflash_verify_probs(torch.zeros(1, 3, 8), torch.zeros(1, 2, 8), i32, i32)
     with pytest.raises(TypeError):
         mm.dflash_verify_probs(torch.zeros(1, 3, 8).half(), torch.zeros(1, 2, 8).half(), i32, i32)
+
+
+def test_verify_probs_workspace_of_refused_sizes(lib):
+    f = lib.dflash_verify_probs_workspace_bytes
+    most_b, most_v = 1 << 20, 1 << 30
+    assert f(1, 1, most_v) > 0 and f(1, 32, most_v) > 0 and f(most_b, 1, 8193) > 0
+    for B, L, V in ((most_b + 1, 1, 8193), (most_b + 1, 1, 3), (2 ** 31 - 1, 1, 50000), (-1, 1, 50000),
+                    (1, 1, most_v + 1), (1, 1, 2 ** 31 - 1), (1, 33, 50000), (1, 0, 50000)):
+        assert f(B, L, V) == 0, (B, L, V)
+        assert lib.dflash_verify_probs(P, P, 0, P, None, P, B, L, V, P, P, P, 1 << 40, None) == -2
