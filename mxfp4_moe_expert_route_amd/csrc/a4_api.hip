@@ -96,6 +96,11 @@ hipError_t product(mxm::a4::Out out, const Problem& p, hipStream_t s) {
 // taller one in a launch of their own: Zipf-routed, 512 tokens take 544 us so
 // and 637 with 32-row tiles alone.  Where there is nothing for it that launch
 // costs about 4 us: small calls and batches with few rows an expert do without.
+// A gate/up item of K below 800 is mostly start and end, which the estimate
+// misses: there the tiled kernel takes over where a typical expert has more rows
+// than a direct unit, 64.  In us, direct and tiled, 384 experts of 2 2048
+// columns, 8 of them a token: K = 544, 8 tokens 22 and 36, 1536 258 and 261, 3040
+// 383 and 298; K = 768, 8 tokens 27 and 29, 8192 859 and 438.
 hipError_t grouped(mxm::a4::Kind kind, mxm::a4::Out out, const Problem& p, hipStream_t s) {
   const bool gu = kind == mxm::a4::kGateUp;
   const int groups = p.R < p.E ? p.R : p.E;
@@ -114,7 +119,7 @@ hipError_t grouped(mxm::a4::Kind kind, mxm::a4::Out out, const Problem& p, hipSt
     const double us = 2.3 + double(ceil_div(units, kCus)) * (0.07 * chunks * frags + 0.8);
     if (us < best) best = us, ms = m;
   }
-  if (mxm::a4::tiled_supported(kind, p)) {
+  if (mxm::a4::tiled_supported(kind, p) && !(gu && p.K < 800 && tall <= 64)) {
     constexpr double kStage[] = {1.35, 1.45, 1.5};   // us per stage of 256 of K
     for (int m = 1; m <= 3; ++m) {
       const int64_t items = groups * ceil_div(tall < 1 ? 1 : tall, 32 * m) * ceil_div(p.N, gu ? 128 : 256);

@@ -58,6 +58,9 @@ constexpr int kRingX = 2;
 constexpr int kMaxE = 1024;
 constexpr uint32_t kDead = 0x80000000u;       // a buffer offset out of every range
 
+// Stages of an item: 256 of K each, in pairs
+__host__ __device__ __forceinline__ int stages(int K) { return 2 * ((K / 32 + 15) / 16); }
+
 template <int AS, int MS>
 struct Lds {
   static constexpr int kNT = 16 * kWN * AS;                 // weight rows per n-tile
@@ -207,7 +210,7 @@ struct Tiled {
     wn = wave % kWN;
     wm = wave / kWN;
     nblk = p.K / 32;
-    nst = 2 * ((nblk + 15) / 16);
+    nst = stages(p.K);
     rowb = p.K / 2;
     wlane = uint32_t(8 * wave + (lane >> 3)) * uint32_t(rowb) + 16u * ((lane & 7) ^ (lane >> 3));
 #pragma unroll
@@ -805,16 +808,17 @@ hipError_t launch_gemm(const Problem& p, int as, int ms, hipStream_t s) {
 }  // namespace
 
 // The kernel addresses activations and one item's weights and outputs by
-// 31-bit byte offsets.  The pair ids of a gate/up item are fetched while the
-// item before it runs its first stage and used two stages before its last:
-// four stages.  Scales are loaded 16 blocks of a row at a time: K >= 512.
+// 31-bit byte offsets.  The pair ids of a gate/up item are fetched behind the
+// barrier of the first stage of the item before it, have landed at the second's
+// and are read behind the last but one's, so an item has to have four stages (K
+// of 544 and more).  Scales are loaded 16 blocks of a row at a time: K >= 512.
 bool tiled_supported(Kind kind, const Problem& p) {
   const int64_t lim = (int64_t(1) << 31) - 1;
   const int64_t rowb = p.K / 2;
   if (p.E > kMaxE || int64_t(p.M) * rowb > lim) return false;
   if (int64_t(kind == kGateUp ? p.N + 256 : 256) * rowb > lim) return false;
   if (int64_t(192) * p.N * 4 > lim || int64_t(p.N) * 2 * (p.K / 32) > lim) return false;
-  return p.K >= (kind == kGateUp ? 800 : 512);
+  return p.K >= 512 && (kind != kGateUp || stages(p.K) >= 4);
 }
 
 hipError_t launch_tiled(Kind kind, Out out, const Problem& p, int ms, bool split, hipStream_t s) {
