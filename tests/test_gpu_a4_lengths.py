@@ -78,3 +78,98 @@ def test_gate_up_short_and_few_rows(mm, T, I, E, k):
         args = (*rand_mx(gen, (T,), H, 124, 127), pairs, offsets, k, *rand_mx(gen, (E, 2 * I), H, 116, 119))
         for call in (mm.moe_mxfp4_a4_gate_up_swiglu, mm.moe_mxfp4_a4_gate_up_swiglu_pack):
             assert [t[0] for t in tiles(lambda: call(*args))] == ["direct"], H
+
+
+# T, H, E, k and the row subtiles of the launches
+DOWN = [(200, 2080, 3, 1, (1,)), (500, 288, 8, 8, (2,)), (500, 544, 32, 8, (3,)),
+        (200, 2080, 384, 8, (3, 1)), (900, 4128, 128, 4, (6, 2)), (900, 4128, 64, 8, (6, 3))]
+
+
+@pytest.mark.parametrize("T,H,E,k,ms", DOWN)
+def test_down(mm, T, H, E, k, ms):
+    for I in LENGTHS:
+        say("down lengths", T, H, I, E, k)
+        gen = torch.Generator(device=DEV).manual_seed(T + H + I + E + k)
+        _, offsets, n = routing(gen, T, E, k, 1.0)
+        lo = lo_scale(I)
+        h, w = rand_mx(gen, (T * k,), I, lo, 127), rand_mx(gen, (E, H), I, lo, 127)
+        assert tiles(lambda: mm.moe_mxfp4_a4_down(*h, offsets, k, *w)) == \
+            [("tiled", 4, m, int(I % 512 == 0)) for m in ms], I
+        y = torch.full((T * k, H), -7.0, device=DEV)
+        mm.moe_mxfp4_a4_down(*h, offsets, k, *w, y=y)
+        off = offsets.tolist()
+        for e in range(0, E, max(1, E // 16)):
+            rows = slice(off[e], off[e + 1])
+            if off[e] < off[e + 1]:
+                want = exact(f64(h[0][rows], h[1][rows]), f64(w[0][e], w[1][e]), lo, lo)
+                assert torch.equal(y[rows].double(), want), (I, e)
+        assert bool((y[n:] == -7).all()) and not bool((y[:n] == -7).all(1).any())
+
+
+GEMM = [(16, 50000, (2, 1), LENGTHS), (700, 2700, (2, 2), LENGTHS), (2100, 1001, (2, 4), LENGTHS),
+        (1500, 2701, (2, 6), LENGTHS), (4537, 2051, (4, 6), range(2048, 2529, 32))]
+
+
+@pytest.mark.parametrize("M,N,tile,lengths", GEMM)
+def test_gemm(mm, M, N, tile, lengths):
+    for K in lengths:
+        say("gemm lengths", M, N, K)
+        gen = torch.Generator(device=DEV).manual_seed(M + N + K)
+        lo = lo_scale(K)
+        a, b = rand_mx(gen, (M,), K, lo, 127), rand_mx(gen, (N,), K, lo, 127)
+        want = exact(f64(*a), f64(*b), lo, lo)
+        for dtype in (torch.float32, torch.bfloat16):
+            assert tiles(lambda: mm.mxfp4_gemm(*a, *b, dtype=dtype)) == [("tiled", *tile, int(K % 512 == 0))], K
+            out = torch.full((M + 2, N), -7.0, device=DEV, dtype=dtype)
+            mm.mxfp4_gemm(*a, *b, dtype=dtype, out=out[1:M + 1])
+            assert torch.equal(out[1:M + 1], want.float().to(dtype)), K
+            assert bool((out[0] == -7).all()) and bool((out[M + 1] == -7).all())
+
+
+# sizes of the direct kernel's units and of the tiles above
+SPECIAL = [(40, 65, "direct"), (60, 1301, "direct"), (40, 2049, "direct"), (100, 2049, "direct"),
+           (16, 50000, "tiled"), (700, 2700, "tiled"), (1500, 2701, "tiled")]
+
+
+@pytest.mark.parametrize("M,N,kernel", SPECIAL)
+def test_gemm_nan_scales(mm, M, N, kernel):
+    """A NaN block makes its row (column) NaN and no other, whatever the block
+    and its neighbours' last and first ones."""
+    for K in LENGTHS:
+        say("gemm lengths, nan", M, N, K)
+        gen = torch.Generator(device=DEV).manual_seed(M + N + K)
+        a, b = rand_mx(gen, (M,), K, 124, 127), rand_mx(gen, (N,), K, 124, 127)
+        assert tiles(lambda: mm.mxfp4_gemm(*a, *b))[0][0] == kernel, K
+        want = exact(f64(*a), f64(*b), 124, 124)
+        last = K // 32 - 1
+        rows, blocks = [1, 2, 4, 9, M - 1], [0, last, 0, 16, last - 1]
+        cols, col_blocks = [0, 17, 18, N // 2, N - 2], [last, 0, last, 15, last // 2]
+        a[1][rows, blocks] = 255
+        b[1][cols, col_blocks] = 255
+        want[rows] = float("nan")
+        want[:, cols] = float("nan")
+        got = mm.mxfp4_gemm(*a, *b).double()
+        assert torch.equal(got.isnan(), want.isnan()), K
+        assert torch.equal(got.nan_to_num(0.0), want.nan_to_num(0.0)), K
+
+
+@pytest.mark.parametrize("M,N,kernel", SPECIAL)
+def test_gemm_zeros_under_the_largest_scales(mm, M, N, kernel):
+    """A zero code times 2^127 times a value under 2^127 is zero, in the blocks
+    of K and in the empty ones past its end."""
+    for K in LENGTHS:
+        say("gemm lengths, zeros under 2^127", M, N, K)
+        gen = torch.Generator(device=DEV).manual_seed(M + N + K)
+        a, b = rand_mx(gen, (M,), K, 124, 127), rand_mx(gen, (N,), K, 124, 127)
+        assert tiles(lambda: mm.mxfp4_gemm(*a, *b))[0][0] == kernel, K
+        b[1][1::3] = 254                             # a third of the columns: 2^127 but in the live blocks
+        for m in (0, 3, M - 1):                      # these rows: zeros but for one block
+            live = (m + K // 32) % (K // 32)
+            for t, fill in ((a[0], 0), (a[1], 254)):
+                keep = t[m].view(K // 32, -1)[live].clone()
+                t[m] = fill
+                t[m].view(K // 32, -1)[live] = keep
+            b[1][1::3, live] = 125
+        want = f64(*a)[[0, 3, M - 1]] @ f64(*b).T
+        got = mm.mxfp4_gemm(*a, *b)[[0, 3, M - 1]].double()
+        assert torch.equal(got, want), K
