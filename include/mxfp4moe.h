@@ -364,7 +364,10 @@ int moe_mxfp4_layer_noalloc(const uint16_t* x_bf16, const float* logits, int T, 
  * Products are exact and accumulated in fp32; bf16 is rounded once at the end
  * (RNE).  Every scale byte is taken as mxfp4_unpack takes it: 0 is 2^-127 and
  * 255 makes the rows (columns) it belongs to NaN; where the products'
- * magnitudes sum past fp32's range the result may be Inf or NaN.
+ * magnitudes sum past fp32's range the result may be Inf or NaN.  Sums and
+ * results keep fp32's (bf16's) subnormals.  Below its normal range fp32 is
+ * spaced 2^-149, and products smaller than that may vanish from a sum one by
+ * one, K 2^-149 in all.
  * Deterministic.  K a multiple of 32 from 32 to 2^20; M and N up to 2^30, 0
  * being a no-op.
  * The pages store weights in MXFP4 (model card, §2 "FP4 Quantization") and
