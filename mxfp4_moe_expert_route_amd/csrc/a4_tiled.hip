@@ -35,14 +35,15 @@
 // end of K load as zero codes.  A row's blocks past its end have scales of that
 // row's own, so a NaN among them is one that the row's result holds anyway.
 //
-// What bounds it.  8192 x 4096 x 6144 takes 127-137 us, 3.0-3.2 PFLOP/s: the
-// products alone, from registers, reach 5.8-6.5 PFLOP/s, and with HBM and LDS
-// busy beside them the clock falls to 1.7-1.9 GHz; a tenth of the time goes to
-// 2.7 rounds of tiles being three.  The page-shaped gate/up (384 experts, 6144 x
-// 2 2048) takes 1.31 ms at 8192 tokens (1.10 at a large copy's rate) and 135 us
-// at 8 (6.1 TB/s, of 7.1 that reads alone reach); down 0.88 ms at 8192 (0.86 at
-// a copy's rate) and 299 us at 64 (6.4 TB/s).  An activation ring of three
-// stages was no faster at any size.
+// What bounds it.  8192 x 4096 x 6144 takes 131-144 us, 2.9-3.1 PFLOP/s.  The
+// matrix pipes are busy a third of its cycles, at 2.1 GHz, and LDS reads a
+// quarter at most, so neither bounds it: what is left are the waits of one
+// workgroup a CU (a barrier a stage, a tile's start and epilogue), and 2.7 rounds
+// of tiles being three.  The page-shaped gate/up (384 experts, 6144 x 2 2048)
+// takes 1.3-1.37 ms at 8192 tokens (1.10 at a large copy's rate; there the clock
+// falls to 1.7 GHz, the pipes busy 39%) and 135 us at 8 (5.9 TB/s; reads alone
+// reach 7.1); down 0.87-0.91 ms at 8192 (0.86 at a copy's rate) and 300 us at 64
+// (6.3 TB/s).  An activation ring of three stages was no faster at any size.
 #include "a4.hpp"
 #include "mx_pack.hpp"
 
@@ -590,6 +591,8 @@ struct Tiled {
     });
     flush_scales();
     __builtin_amdgcn_s_waitcnt(MXM_LGKM0);
+    // (the tiles that reload spilled registers at an item's start have waited
+    // for the stores by then)
     if constexpr (FIRST) vmcnt_le(L::kWLoads + stores);
     else __builtin_amdgcn_s_waitcnt(MXM_VMCNT(L::kWLoads));
     wg_barrier();
@@ -764,8 +767,12 @@ hipError_t launch(const Problem& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Where K is not whole, 192 rows of gate/up leave no registers to bring scales
-// to their places (spills in the main loop); 160 do.
+// Tiles of 192 rows use every register.  With K whole they spill 18 to 34: gate/up
+// and down at the start of an item, the product also in its main loop, the second
+// of a wave's two scale loads on its way to LDS, out and back once in four stages.
+// A reload waits for every load in flight.  Where K is not whole products and
+// down spill at most three, not in the loop; gate/up has none left to bring scales
+// to their places, and takes 160 rows, without spills.
 template <Kind KIND, Out OUT, int AS, int MS>
 hipError_t launch_k(const Problem& p, hipStream_t s) {
   const bool whole = p.K % 512 == 0 && reinterpret_cast<uintptr_t>(p.xs) % 16 == 0 &&
