@@ -383,12 +383,14 @@ int mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b
  *   sorted_pairs, offsets, w13_codes, w13_scales: as there
  *   h_bf16  [T*k, I] bf16, written as there; or NULL, and then
  *   h_codes [T*k, I/2], h_scales [T*k, I/32] uint8, written: mxfp4_pack of
- *           that h (of its bf16 values), bit for bit.  Exactly one of h_bf16
- *           and the pair is given; anything else is MXM_ERR_NULL.
+ *           the h_r below (of its bf16 values).  Exactly one of h_bf16 and
+ *           the pair is given; anything else is MXM_ERR_NULL.
  * For row r of expert e with token t = sorted_pairs[r] / k: g = W_gate,e x_t
  * and u = W_up,e x_t with exact products accumulated in fp32, h_r =
  * bf16_rne(silu(g) * u).  Scale bytes as mxfp4_gemm takes them (0 and 255
- * included, unlike the bf16-activation call).  Rows at and past offsets[E]
+ * included, unlike the bf16-activation call).  The two forms may run kernels
+ * that add in different orders: where fp32 rounds the sums, so may their h.
+ * Each form is deterministic.  Rows at and past offsets[E]
  * are left as they were.  Codes and h 16-byte aligned, scales unaligned.
  */
 int moe_mxfp4_a4_gate_up_swiglu(const uint8_t* x_codes, const uint8_t* x_scales,

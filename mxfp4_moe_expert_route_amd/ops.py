@@ -431,7 +431,8 @@ def moe_mxfp4_a4_gate_up_swiglu(x_codes, x_scales, sorted_pairs, offsets, k, w13
 def moe_mxfp4_a4_gate_up_swiglu_pack(x_codes, x_scales, sorted_pairs, offsets, k, w13_codes,
                                      w13_scales, h_codes=None, h_scales=None):
     """moe_mxfp4_a4_gate_up_swiglu writing h in MXFP4 (mxfp4_pack of the
-    bfloat16 h, bit for bit) -> (h_codes [T*k, I/2], h_scales [T*k, I/32])."""
+    bfloat16 h; where the sums are rounded in fp32 this call may round them in
+    another order than that one) -> (h_codes [T*k, I/2], h_scales [T*k, I/32])."""
     T, H, I, E, dev = _a4_gate_up_shapes(x_codes, x_scales, sorted_pairs, offsets, k, w13_codes,
                                          w13_scales)
     h_codes = _result(h_codes, "h_codes", torch.uint8, (T * k, I // 2), dev)
