@@ -63,6 +63,8 @@ enum mxm_status {
 
 enum mxm_dtype { MXM_F32 = 0, MXM_BF16 = 1 };
 
+enum mxm_score { MXM_SCORE_SOFTMAX = 0, MXM_SCORE_SIGMOID = 1 };
+
 /* Library version as 10000*major + 100*minor + patch. */
 int mxm_version(void);
 
@@ -462,6 +464,102 @@ int dflash_verify_probs(const void* target_probs, const void* draft_probs, int d
                         const float* uniforms, int B, int L, int V, int32_t* accept_len,
                         int32_t* next_token, void* workspace, size_t workspace_bytes,
                         void* stream);
+
+/*
+ * moe_route_scored — choose k experts per token by scores, a bias and groups.
+ *   logits  [T, E] f32, read
+ *   bias    [E] f32 added to the scores for the choice alone, read; may be NULL
+ *   score   MXM_SCORE_SOFTMAX: s = softmax of the row over its E experts;
+ *           MXM_SCORE_SIGMOID: s_e = 1 / (1 + exp(-l_e))
+ *   groups, topk_groups, group_best: the experts form `groups` runs of E/groups
+ *           (1 <= groups <= 64, E % groups == 0).  A group's value is the sum
+ *           of its group_best (1 or 2; all, where it has fewer) largest
+ *           available c = s + bias, and only the topk_groups groups of the
+ *           largest values take part; groups = topk_groups = 1 for none
+ *   renormalise  0: weights are the scores; else s_j / sum_j' s_j' of the chosen
+ *   scale   finite factor of the weights
+ *   topk_ids[T, k] int32, written: available experts of these groups by
+ *           descending c (by descending logit where bias is NULL, which is the
+ *           same order), the lower index first on equal values
+ *   topk_w  [T, k] f32, written
+ * Logits or values c that are NaN or -Inf make an expert unavailable.  Where
+ * fewer than k are left, the rest of the row is id -1 with weight 0 (which
+ * moe_permute drops and moe_combine skips): a row without any available expert
+ * is -1 throughout.  Logits of the largest negative number are available.
+ * +Inf logits share a softmax row among themselves; their sigmoid is 1.
+ * Values c are compared in fp64 (a group's sum, too); one that lies within
+ * fp64's rounding of another may be taken for equal or for the other side.
+ * Renormalised weights hold where every chosen score underflows.  Weights are
+ * within 2^-21 of the rule's, relative (below fp32's normal range 2^-149,
+ * absolute).  Deterministic.  1 <= k <= min(32, topk_groups E/groups),
+ * E <= 1024; an unknown score is MXM_ERR_DTYPE, all else MXM_ERR_SHAPE.
+ * The pages give 384 experts with 8 active per token and no scoring rule; these
+ * are the rules of layers that balance experts by a bias or keep tokens to a
+ * few groups of them.
+ */
+int moe_route_scored(const float* logits, const float* bias, int T, int E, int k, int score,
+                     int groups, int topk_groups, int group_best, int renormalise, float scale,
+                     int32_t* topk_ids, float* topk_w, void* stream);
+
+/*
+ * moe_route_scored_permute — moe_route_scored followed by moe_permute, in one
+ * call (one launch for T <= 16).  Arguments and workspace as those two calls;
+ * results are theirs, bit for bit.
+ */
+int moe_route_scored_permute(const float* logits, const float* bias, int T, int E, int k,
+                             int score, int groups, int topk_groups, int group_best,
+                             int renormalise, float scale, int32_t* topk_ids, float* topk_w,
+                             int32_t* counts, int32_t* offsets, int32_t* sorted_pairs,
+                             int32_t* pair_to_row, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * moe_mxfp4_scored_layer — moe_mxfp4_layer with the routing of
+ * moe_route_scored: enqueues moe_route_scored_permute,
+ * moe_mxfp4_gate_up_swiglu, moe_mxfp4_down and moe_combine, with the caller's
+ * buffers as there.  Results are those of the separate calls, bit for bit;
+ * rows of h and y at and past offsets[E] are left as they were, and a token
+ * without an available expert gets zeros.
+ */
+int moe_mxfp4_scored_layer(const uint16_t* x_bf16, const float* logits, const float* bias, int T,
+                           int H, int I, int E, int k, int score, int groups, int topk_groups,
+                           int group_best, int renormalise, float scale,
+                           const uint8_t* w13_codes, const uint8_t* w13_scales,
+                           const uint8_t* w2_codes, const uint8_t* w2_scales, int32_t* topk_ids,
+                           float* topk_w, int32_t* counts, int32_t* offsets,
+                           int32_t* sorted_pairs, int32_t* pair_to_row, uint16_t* h_bf16,
+                           float* y, float* out, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* Workspace lora_add needs (0 for invalid sizes and empty problems). */
+size_t lora_add_workspace_bytes(int M, int K, int N, int S, int r);
+
+/*
+ * lora_add — low-rank adapters of many requests, added to the result of a
+ * projection that they share (mxfp4_gemm, moe_router_topk's logits):
+ *   y[m, n] += scale[s] * sum_j b[s, n, j] * sum_k a[s, j, k] * x[m, k]
+ * for every row m of every adapter s.
+ *   x_bf16      [M, K] bf16, read; the projection's input
+ *   sorted_rows [M], offsets [S+1] int32, read: the rows by adapter, from
+ *               moe_permute(slots, M, S, 1, ...) of the rows' adapters.  Rows
+ *               whose slot is outside [0, S) are dropped there and stay as they
+ *               were here.  A row is listed once
+ *   a_bf16      [S, r, K], b_bf16 [S, N, r] bf16, read
+ *   scale       [S] f32, read; may be NULL (1)
+ *   y           [M, N] f32 or bf16 (y_dtype), read and written; aligned to its
+ *               elements
+ *   workspace   lora_add_workspace_bytes(M, K, N, S, r) bytes, 16-byte
+ *               aligned; its contents need no initialisation.  Calls that
+ *               share one must not overlap
+ * Products are exact and sums, the scaled a x among them, are fp32; a bf16 y
+ * is rounded once (RNE).  Deterministic.  K a multiple of 8 up to 2^17, N up to
+ * 2^17, M up to 2^20, S up to 1024, r up to 128; x, a and b 16-byte aligned.
+ * Not on the pages: serving many fine-tuned variants of one set of weights.
+ */
+int lora_add(const uint16_t* x_bf16, const int32_t* sorted_rows, const int32_t* offsets, int M,
+             int K, int N, int S, int r, const uint16_t* a_bf16, const uint16_t* b_bf16,
+             const float* scale, void* y, int y_dtype, void* workspace, size_t workspace_bytes,
+             void* stream);
 
 /*
  * mxm_stream_xor — measurement aid, not a step of the layer: a plain

@@ -13,6 +13,7 @@ from .ops import (  # noqa: F401
     mxfp4_unpack, mxm_stream_xor,
     A4LayerBuffers, dflash_verify_probs, dflash_verify_probs_workspace_bytes, moe_mxfp4_a4_down,
     moe_mxfp4_a4_gate_up_swiglu, moe_mxfp4_a4_gate_up_swiglu_pack, moe_mxfp4_a4_layer, mxfp4_gemm,
+    lora_add, lora_add_workspace_bytes, moe_mxfp4_scored_layer, moe_route_scored, moe_route_scored_permute,
 )
 
 MXM_F32, MXM_BF16 = 0, 1

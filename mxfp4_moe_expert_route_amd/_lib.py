@@ -9,6 +9,7 @@ import os
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmxfp4moe.so")
 
+_c_float = ctypes.c_float
 _c_int, _c_i64, _c_size, _p = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
 
 # name -> (restype, argtypes); mirrors include/mxfp4moe.h
@@ -48,6 +49,13 @@ SIGNATURES = {
     "dflash_verify_probs_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int]),
     "dflash_verify_probs": (_c_int, [_p, _p, _c_int, _p, _p, _p, _c_int, _c_int, _c_int, _p, _p,
                                      _p, _c_size, _p]),
+    "moe_route_scored": (_c_int, [_p, _p] + [_c_int] * 8 + [_c_float, _p, _p, _p]),
+    "moe_route_scored_permute": (_c_int, [_p, _p] + [_c_int] * 8 + [_c_float] + [_p] * 7
+                                 + [_c_size, _p]),
+    "moe_mxfp4_scored_layer": (_c_int, [_p, _p, _p] + [_c_int] * 10 + [_c_float] + [_p] * 14
+                               + [_c_size, _p]),
+    "lora_add_workspace_bytes": (_c_size, [_c_int] * 5),
+    "lora_add": (_c_int, [_p, _p, _p] + [_c_int] * 5 + [_p, _p, _p, _p, _c_int, _p, _c_size, _p]),
     "moe_mxfp4_layer": (_c_int, [_p, _p, _c_int, _c_int, _c_int, _c_int, _c_int, _p, _p, _p, _p,
                                  _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _c_size, _p]),
 }

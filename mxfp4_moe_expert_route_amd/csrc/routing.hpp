@@ -259,8 +259,9 @@ __device__ __forceinline__ void permute_block(const int32_t* ids, int r0, int r1
 // when `tiles` is set, tile i (the i-th expert with pairs, in expert order)
 // gets {e | count << 16, offsets[e]} and *ntiles the number of tiles.  ids
 // [R] and mask [E] are in LDS; off_lds is an LDS copy of offsets [E + 1]; the
-// other outputs may be global or LDS.
-template <int NW>
+// other outputs may be global or LDS.  Drops: ids may be -1 (no bit in any
+// mask), and such a pair's pair_to_row is -1.
+template <int NW, bool Drops = false>
 __device__ __forceinline__ void group_small(const int32_t* ids, const uint32_t* mask, int R,
                                             int E, int k, int32_t* counts, int32_t* offsets,
                                             int32_t* off_lds, int32_t* sorted_pairs,
@@ -311,6 +312,12 @@ __device__ __forceinline__ void group_small(const int32_t* ids, const uint32_t* 
   __syncthreads();
   for (int p = tid; p < R; p += NT) {
     const int t = p / k, e = ids[p];
+    if constexpr (Drops) {
+      if (e < 0) {
+        pair_to_row[p] = -1;
+        continue;
+      }
+    }
     const int row = off_lds[e] + __popc(mask[e] & ((1u << t) - 1u));
     sorted_pairs[row] = p;
     pair_to_row[p] = row;

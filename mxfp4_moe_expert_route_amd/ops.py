@@ -539,6 +539,125 @@ def dflash_verify_probs(target_probs, draft_probs, draft_tokens, uniforms, draft
     return accept_len, next_token
 
 
+# ---- routing by scores, and low-rank adapters -------------------------------
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score_code(score):
+    code = _SCORES.get(score)
+    if code is None:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    return code
+
+
+def moe_route_scored(logits, k, bias=None, score="sigmoid", groups=1, topk_groups=1, group_best=2,
+                     renormalise=True, scale=1.0, topk_ids=None, topk_w=None):
+    """logits [T, E] float32 (bias [E] float32 or None) -> (ids int32 [T, k],
+    weights float32 [T, k]): the best k by score + bias among the experts of
+    the topk_groups best groups; id -1 and weight 0 where fewer are available."""
+    T, E = _rank(logits, "logits", 2)
+    dev, code = logits.device, _score_code(score)
+    _want(logits, "logits", torch.float32, (T, E), dev)
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (E,), dev)
+    topk_ids = _result(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+    topk_w = _result(topk_w, "topk_w", torch.float32, (T, k), dev)
+    _enqueue("moe_route_scored", dev, logits.data_ptr(), None if bias is None else bias.data_ptr(),
+             T, E, k, code, groups, topk_groups, group_best, 1 if renormalise else 0, scale,
+             topk_ids.data_ptr(), topk_w.data_ptr())
+    return topk_ids, topk_w
+
+
+def moe_route_scored_permute(logits, k, bias=None, score="sigmoid", groups=1, topk_groups=1,
+                             group_best=2, renormalise=True, scale=1.0, topk_ids=None, topk_w=None,
+                             counts=None, offsets=None, sorted_pairs=None, pair_to_row=None,
+                             workspace=None):
+    """moe_route_scored then moe_permute in one call -> (topk_ids [T, k],
+    topk_w [T, k], counts [E], offsets [E+1], sorted_pairs [T*k], pair_to_row [T*k])."""
+    T, E = _rank(logits, "logits", 2)
+    dev, code = logits.device, _score_code(score)
+    _want(logits, "logits", torch.float32, (T, E), dev)
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (E,), dev)
+    topk_ids = _result(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+    topk_w = _result(topk_w, "topk_w", torch.float32, (T, k), dev)
+    counts = _result(counts, "counts", torch.int32, (E,), dev)
+    offsets = _result(offsets, "offsets", torch.int32, (E + 1,), dev)
+    sorted_pairs = _result(sorted_pairs, "sorted_pairs", torch.int32, (T * k,), dev)
+    pair_to_row = _result(pair_to_row, "pair_to_row", torch.int32, (T * k,), dev)
+    if workspace is None:
+        need = moe_permute_workspace_bytes(T, E, k)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        _need(workspace, "workspace", torch.uint8, None, dev)
+    _enqueue("moe_route_scored_permute", dev, logits.data_ptr(),
+             None if bias is None else bias.data_ptr(), T, E, k, code, groups, topk_groups,
+             group_best, 1 if renormalise else 0, scale, topk_ids.data_ptr(), topk_w.data_ptr(),
+             counts.data_ptr(), offsets.data_ptr(), sorted_pairs.data_ptr(), pair_to_row.data_ptr(),
+             _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return topk_ids, topk_w, counts, offsets, sorted_pairs, pair_to_row
+
+
+def moe_mxfp4_scored_layer(x, logits, k, w13_codes, w13_scales, w2_codes, w2_scales, bias=None,
+                           score="sigmoid", groups=1, topk_groups=1, group_best=2,
+                           renormalise=True, scale=1.0, buffers=None):
+    """moe_mxfp4_layer with the routing of moe_route_scored, in one C call.
+
+    Returns the LayerBuffers holding every intermediate; `.out` is the result."""
+    T, H = _rank(x, "x", 2)
+    E, two_i, _ = _rank(w13_codes, "w13_codes", 3)
+    I, dev, code = two_i // 2, x.device, _score_code(score)
+    _want(x, "x", torch.bfloat16, (T, H), dev)
+    _want(logits, "logits", torch.float32, (T, E), dev)
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (E,), dev)
+    _need_mx(w13_codes, w13_scales, "w13", (E, 2 * I, H), dev)
+    _need_mx(w2_codes, w2_scales, "w2", (E, H, I), dev)
+    b = buffers if buffers is not None else LayerBuffers(T, H, I, E, k, dev)
+    if (b.T, b.H, b.I, b.E, b.k) != (T, H, I, E, k) or b.out.device != dev:
+        raise ValueError("buffers were made for another shape or device")
+    _enqueue("moe_mxfp4_scored_layer", dev, _ptr(x), _ptr(logits), _ptr(bias), T, H, I, E, k, code,
+             groups, topk_groups, group_best, 1 if renormalise else 0, scale, _ptr(w13_codes),
+             _ptr(w13_scales), _ptr(w2_codes), _ptr(w2_scales), _ptr(b.topk_ids), _ptr(b.topk_w),
+             _ptr(b.counts), _ptr(b.offsets), _ptr(b.sorted_pairs), _ptr(b.pair_to_row), _ptr(b.h),
+             _ptr(b.y), _ptr(b.out), _ptr(b.workspace), b.workspace.numel())
+    return b
+
+
+def lora_add_workspace_bytes(M, K, N, S, r):
+    return int(lib().lora_add_workspace_bytes(M, K, N, S, r))
+
+
+def lora_add(x, sorted_rows, offsets, a, b, y, scale=None, workspace=None):
+    """y [M, N] (float32 or bfloat16) += scale_s * (x A_s^T) B_s^T for the rows of
+    every adapter s, in place: x [M, K] bfloat16, a [S, r, K] and b [S, N, r]
+    bfloat16, scale [S] float32 or None, and the rows by adapter, sorted_rows [M]
+    and offsets [S+1] int32, from moe_permute(slots [M, 1], S).  Returns y."""
+    M, K = _rank(x, "x", 2)
+    S, r, _ = _rank(a, "a", 3)
+    N = _rank(y, "y", 2)[1]
+    dev, dtype = x.device, y.dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("y must be float32 or bfloat16")
+    _want(x, "x", torch.bfloat16, (M, K), dev)
+    _want(sorted_rows, "sorted_rows", torch.int32, (M,), dev)
+    _want(offsets, "offsets", torch.int32, (S + 1,), dev)
+    _want(a, "a", torch.bfloat16, (S, r, K), dev)
+    _want(b, "b", torch.bfloat16, (S, N, r), dev)
+    _want(y, "y", dtype, (M, N), dev)
+    if scale is not None:
+        _want(scale, "scale", torch.float32, (S,), dev)
+    if workspace is None:
+        workspace = torch.empty(lora_add_workspace_bytes(M, K, N, S, r), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, None, dev)
+    _enqueue("lora_add", dev, x.data_ptr(), sorted_rows.data_ptr(), offsets.data_ptr(), M, K, N, S, r,
+             a.data_ptr(), b.data_ptr(), None if scale is None else scale.data_ptr(), y.data_ptr(),
+             BF16 if dtype == torch.bfloat16 else F32, _ptr(workspace), workspace.numel())
+    return y
+
+
 def mxm_stream_xor(src, result, nontemporal=False):
     """Streaming-read probe (a measurement aid): XOR every 32-bit word of the
     contiguous tensor `src` (byte size a multiple of 16) into `result`, an
