@@ -13,9 +13,13 @@
 // the taken, times `scale`.  Where fewer than k are available the rest of the
 // row is id -1 with weight 0.
 //
-// Choices compare values of 64 bits: c next to 1 saturates in 32, and a choice
-// that a rounding decides would differ between two ways to compute the same
-// rule.
+// Choices are those of 64 bits: c next to 1 saturates in 32, and a choice that a
+// rounding decides would differ between two ways to compute the same rule.  But
+// 32 bits tell nearly every pair of values apart, so a wave first chooses by
+// fp32 values whose error it knows, and keeps that choice if every two
+// successive values (and the last taken and the first left) are further apart
+// than their errors; otherwise it chooses again in fp64.  8192 tokens of 384
+// experts in 8 groups: 16 us, 36 in fp64 throughout.
 #pragma once
 #include "routing.hpp"
 
@@ -32,7 +36,8 @@ struct ScoreRule {
 
 hipError_t launch_route_scored(const float* logits, const float* bias, int T, const ScoreRule& r,
                                int32_t* ids, float* w, hipStream_t s);
-// routing and grouping in one workgroup: T <= 16
+// routing and grouping in one workgroup, where it fits
+bool route_scored_fusable(int T, const ScoreRule& r);
 hipError_t launch_route_scored_permute(const float* logits, const float* bias, int T,
                                        const ScoreRule& r, int32_t* ids, float* w,
                                        int32_t* counts, int32_t* offsets, int32_t* sorted_pairs,
@@ -47,61 +52,92 @@ __device__ __forceinline__ uint64_t order_key64(double v) {
 
 __device__ __forceinline__ double max_f64(double a, double b) { return a > b ? a : b; }
 
-__device__ __forceinline__ double wave_max_f64(double v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) v = max_f64(v, __shfl_xor(v, d));
-  return v;
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  auto up = [&](int x) { v = max(v, uint32_t(x)); };
+  up(__builtin_amdgcn_update_dpp(0, int(v), 0x111, 0xf, 0xf, true));   // row_shr:1
+  up(__builtin_amdgcn_update_dpp(0, int(v), 0x112, 0xf, 0xf, true));   // row_shr:2
+  up(__builtin_amdgcn_update_dpp(0, int(v), 0x114, 0xf, 0xf, true));   // row_shr:4
+  up(__builtin_amdgcn_update_dpp(0, int(v), 0x118, 0xf, 0xf, true));   // row_shr:8
+  up(__builtin_amdgcn_update_dpp(0, int(v), 0x142, 0xa, 0xf, true));   // row_bcast:15
+  up(__builtin_amdgcn_update_dpp(0, int(v), 0x143, 0xc, 0xf, true));   // row_bcast:31
+  return uint32_t(__builtin_amdgcn_readlane(int(v), kWave - 1));
 }
 
+// Sum over the wave in fp64, in the order of wave_sum_f32.
 __device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d);
-  return v;
+  auto add = [&](uint64_t x) { v += __longlong_as_double((long long)x); };
+  add(dpp_u64<0x111, 0xf>(uint64_t(__double_as_longlong(v))));
+  add(dpp_u64<0x112, 0xf>(uint64_t(__double_as_longlong(v))));
+  add(dpp_u64<0x114, 0xf>(uint64_t(__double_as_longlong(v))));
+  add(dpp_u64<0x118, 0xf>(uint64_t(__double_as_longlong(v))));
+  add(dpp_u64<0x142, 0xa>(uint64_t(__double_as_longlong(v))));
+  add(dpp_u64<0x143, 0xc>(uint64_t(__double_as_longlong(v))));
+  const uint64_t u = uint64_t(__double_as_longlong(v));
+  const uint32_t lo = __builtin_amdgcn_readlane(int(uint32_t(u)), kWave - 1);
+  const uint32_t hi = __builtin_amdgcn_readlane(int(uint32_t(u >> 32)), kWave - 1);
+  return __longlong_as_double((long long)((uint64_t(hi) << 32) | lo));
 }
 
-__device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
+// v of lane ^ D where the lanes of each run of D already agree (D = 4 and 8
+// mirror a run of 2 D)
+template <int D>
+__device__ __forceinline__ float across(float v) {
+  if constexpr (D == 1) return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xb1, 0xf, 0xf, true));
+  if constexpr (D == 2) return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4e, 0xf, 0xf, true));
+  if constexpr (D == 4) return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xf, 0xf, true));
+  if constexpr (D == 8) return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xf, 0xf, true));
+  return __shfl_xor(v, D);
+}
 
-// One token by one whole wave.  Lane (g << lanes_log2) + m holds the experts
-// m, m + lanes, ... of group g, at most NPER of them, so a group's largest
-// values meet in log2(lanes) steps for all groups at once.  Lanes 0..k-1 end
-// with the j-th choice and its weight.
+// exp(x) for x <= 0 to 2^-22, relative: the argument's product and its whole
+// part in fp64, so that its size does not count.  Below fp32's range 0.
+__device__ __forceinline__ float exp_down(double x) {
+  const double t = x * 1.4426950408889634;
+  const double n = rint(t);
+  const float e = __builtin_ldexpf(__builtin_amdgcn_exp2f(float(t - n)), x > -120.0 ? int(n) : 0);
+  return x > -120.0 ? e : 0.f;
+}
+
+__device__ __forceinline__ float lane_f32(float v, int src) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), src));
+}
+
+// Where a lane's experts are: lane (g << lanes_log2) + m holds the experts m,
+// m + lanes, ... of group g, at most NPER of them, so a group's largest values
+// meet in log2(lanes) steps for all groups at once.
+struct ScorePlace {
+  int lane, lanes, g, m;
+  int e0;                                         // slot i holds expert e0 + lanes * i
+  __device__ explicit ScorePlace(const ScoreRule& r)
+      : lane(lane_id()), lanes(1 << r.lanes_log2), g(lane >> r.lanes_log2), m(lane & (lanes - 1)),
+        e0(g * r.size + m) {}
+};
+
+// The choice in fp64; lanes 0..k-1 end with the j-th id, or -1.  v is NaN in
+// slots without an expert, top the row's largest logit.
 template <int NPER>
-__device__ __forceinline__ void score_token(const float* __restrict__ row,
-                                            const float* __restrict__ bias, const ScoreRule& r,
-                                            int& my_id, float& my_w) {
+__device__ __forceinline__ int choose_f64(const float (&v)[NPER], const float (&b)[NPER],
+                                          bool biased, float top, const ScoreRule& r,
+                                          const ScorePlace& at) {
   const double none = -__builtin_inf();
-  const int lane = lane_id();
-  const int lanes = 1 << r.lanes_log2;
-  const int g = lane >> r.lanes_log2, m = lane & (lanes - 1);
-  const int e0 = g * r.size + m;                  // slot i holds expert e0 + lanes * i
-  float v[NPER], b[NPER];
-#pragma unroll
-  for (int i = 0; i < NPER; ++i) {
-    const bool in = g < r.groups && m + lanes * i < r.size;
-    v[i] = row[in ? e0 + lanes * i : 0];
-    b[i] = bias ? bias[in ? e0 + lanes * i : 0] : 0.f;
-    if (!in) v[i] = __builtin_nanf("");
-  }
-  // scores; c[i] = -inf: not available
-  double c[NPER];
-  double top = none, total = 0.0;
-#pragma unroll
-  for (int i = 0; i < NPER; ++i) top = v[i] > top ? double(v[i]) : top;
-  top = wave_max_f64(top);
+  double c[NPER];                                 // -inf: not available
+  double total = 0.0;
 #pragma unroll
   for (int i = 0; i < NPER; ++i) {
     const double l = v[i];
-    const double s = r.sigmoid ? sigmoid64(l) : (l == top ? 1.0 : exp(l - top));
+    const double s = r.sigmoid ? 1.0 / (1.0 + exp(-l)) : v[i] == top ? 1.0 : exp(l - double(top));
     c[i] = l > none ? s : 0.0;
     total += c[i];
+    __builtin_amdgcn_sched_barrier(0);            // one at a time: few registers
   }
   total = wave_sum_f64(total);
 #pragma unroll
   for (int i = 0; i < NPER; ++i) {
     c[i] = (r.sigmoid ? c[i] : c[i] / total) + double(b[i]);
-    if (!(v[i] > none) || !(c[i] > none)) c[i] = none;
+    if (!(double(v[i]) > none) || !(c[i] > none)) c[i] = none;
+    __builtin_amdgcn_sched_barrier(0);
   }
-  bool kept = g < r.groups;
+  bool kept = at.g < r.groups;
   if (r.groups > 1) {
     double a1 = none, a2 = none;                  // the two largest of the group
 #pragma unroll
@@ -109,7 +145,7 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
       a2 = c[i] > a1 ? a1 : max_f64(a2, c[i]);
       a1 = max_f64(a1, c[i]);
     }
-    for (int d = 1; d < lanes; d <<= 1) {
+    for (int d = 1; d < at.lanes; d <<= 1) {
       const double o1 = __shfl_xor(a1, d), o2 = __shfl_xor(a2, d);
       a2 = o1 > a1 ? max_f64(a1, o2) : max_f64(a2, o1);
       a1 = max_f64(a1, o1);
@@ -118,52 +154,207 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
     int before = 0;
     for (int j = 0; j < r.groups; ++j) {
       const double o = __shfl(value, j << r.lanes_log2);
-      before += o > value || (o == value && j < g);
+      before += o > value || (o == value && j < at.g);
     }
     kept = kept && before < r.keep;
   }
   uint64_t key[NPER];
 #pragma unroll
   for (int i = 0; i < NPER; ++i)
-    key[i] = kept && c[i] > none ? order_key64(bias ? c[i] : double(v[i])) : 0ull;
-  my_id = -1;
-  float my_l = 0.f;
-  int taken = 0;
+    key[i] = kept && c[i] > none ? order_key64(biased ? c[i] : double(v[i])) : 0ull;
+  int my_id = -1;
   for (int j = 0; j < r.k; ++j) {
     uint64_t mine = key[0];
-    int e = e0;
-    float l = v[0];
+    int e = at.e0;
 #pragma unroll
     for (int i = 1; i < NPER; ++i)
-      if (key[i] > mine) mine = key[i], e = e0 + lanes * i, l = v[i];
+      if (key[i] > mine) mine = key[i], e = at.e0 + at.lanes * i;
     const uint64_t best = wave_max_u64(mine);
     if (best == 0ull) break;                      // no available expert is left
-    int first = mine == best ? e : 0x7fffffff;
+    const unsigned long long owners = __ballot(mine == best);
+    int first;
+    if (__popcll(owners) == 1) {
+      first = __builtin_amdgcn_readlane(e, __ffsll((long long)owners) - 1);
+    } else {
+      first = mine == best ? e : 0x7fffffff;
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) first = min(first, __shfl_xor(first, d));
-    const unsigned long long owner = __ballot(mine == best && e == first);
-    const float chosen = __shfl(l, __ffsll((long long)owner) - 1);
+      for (int d = 1; d < kWave; d <<= 1) first = min(first, __shfl_xor(first, d));
+    }
 #pragma unroll
     for (int i = 0; i < NPER; ++i)
-      if (e0 + lanes * i == first && key[i] == best) key[i] = 0ull;
-    if (lane == j) my_id = first, my_l = chosen;
-    ++taken;
+      if (at.e0 + at.lanes * i == first && mine == best) key[i] = 0ull;
+    if (at.lane == j) my_id = first;
   }
-  // weights: renormalised ones are a softmax of log s over the taken, so that
-  // they hold where every s underflows
-  const bool has = lane < taken;
-  const double l = my_l;
-  double p;
-  if (r.norm) {
-    const double z = !has ? none : r.sigmoid ? fmin(l, 0.0) - log1p(exp(-fabs(l))) : l;
-    const double zm = wave_max_f64(z);
-    p = !has ? 0.0 : z == zm ? 1.0 : exp(z - zm);
-    const double sum = wave_sum_f64(p);
-    p = has ? p / sum : 0.0;
+  return my_id;
+}
+
+// Descending order of N values by a fixed network (odd-even merges of the next
+// power of two, without the places past N).
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&key)[N]) {
+  constexpr int P = N <= 2 ? 2 : N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : 32;
+#pragma unroll
+  for (int p = 1; p < P; p *= 2)
+#pragma unroll
+    for (int d = p; d >= 1; d /= 2)
+#pragma unroll
+      for (int j = d % p; j + d < P; j += 2 * d)
+#pragma unroll
+        for (int i = 0; i < d; ++i) {
+          const int x = i + j, y = i + j + d;
+          if (y < N && x / (2 * p) == y / (2 * p)) {
+            const uint32_t hi = max(key[x], key[y]), lo = min(key[x], key[y]);
+            key[x] = hi;
+            key[y] = lo;
+          }
+        }
+}
+
+// One token by one whole wave; lanes 0..k-1 end with the j-th choice and its
+// weight.
+template <int NPER>
+__device__ __forceinline__ void score_token(const float* __restrict__ row,
+                                            const float* __restrict__ bias, const ScoreRule& r,
+                                            int& my_id, float& my_w) {
+  constexpr int SB = NPER <= 2 ? 1 : NPER <= 4 ? 2 : NPER <= 8 ? 3 : NPER <= 16 ? 4 : 5;
+  constexpr uint32_t kSlots = (1u << SB) - 1u;
+  const float none = -__builtin_inff();
+  const ScorePlace at(r);
+  float v[NPER], b[NPER];
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) {
+    const bool in = at.g < r.groups && at.m + at.lanes * i < r.size;
+    v[i] = row[in ? at.e0 + at.lanes * i : 0];
+    b[i] = bias ? bias[in ? at.e0 + at.lanes * i : 0] : 0.f;
+    if (!in) v[i] = __builtin_nanf("");
+  }
+  // fp32 values and a bound on the scores' error
+  float top = none, total = 1.f;
+  if (!r.sigmoid) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) t = max(t, v[i] > none ? order_key(v[i]) : 0u);
+    t = wave_max_u32(t);
+    top = t ? key_value(t) : none;
+  }
+  const bool scored = bias || r.groups > 1;       // else logits decide
+  float c[NPER], ds = 0.f;
+  if (r.sigmoid) {
+    // |error| of s: s (1 - s) (1.5 2^-24 |l| + 2^-23) of the exponential and 1.5
+    // 2^-23 s of the sum and the reciprocal, below 2^-22
+    ds = 0x1p-21f;
+#pragma unroll
+    for (int i = 0; i < NPER; ++i)
+      c[i] = scored ? __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v[i] * -1.4426950408889634f)) : 0.f;
+  } else if (scored || !r.norm) {
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+      c[i] = !(v[i] > none) ? 0.f : v[i] == top ? 1.f : exp_down(double(v[i]) - double(top));
+      sum += double(c[i]);
+    }
+    total = float(wave_sum_f64(sum));
+    const float inv = __builtin_amdgcn_rcpf(total);
+    ds = 0x1p-20f * inv;                          // each s is at most 1 / total
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) c[i] *= inv;
   } else {
-    p = !has ? 0.0 : r.sigmoid ? sigmoid64(l) : (l == top ? 1.0 : exp(l - top)) / total;
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) c[i] = 0.f;
   }
-  my_w = float(p * double(r.scale));
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) {
+    c[i] += b[i];
+    if (!(v[i] > none) || !(c[i] > none)) c[i] = none;
+  }
+  bool kept = at.g < r.groups, doubt = false;
+  if (r.groups > 1) {
+    float a1 = none, a2 = none;                   // the two largest of the group
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+      a2 = fmaxf(a2, fminf(a1, c[i]));
+      a1 = fmaxf(a1, c[i]);
+    }
+    auto meet = [&](float o1, float o2) {
+      a2 = fmaxf(fminf(a1, o1), fmaxf(a2, o2));
+      a1 = fmaxf(a1, o1);
+    };
+    if (r.lanes_log2 > 0) meet(across<1>(a1), across<1>(a2));
+    if (r.lanes_log2 > 1) meet(across<2>(a1), across<2>(a2));
+    if (r.lanes_log2 > 2) meet(across<4>(a1), across<4>(a2));
+    if (r.lanes_log2 > 3) meet(across<8>(a1), across<8>(a2));
+    if (r.lanes_log2 > 4) meet(across<16>(a1), across<16>(a2));
+    const bool two = r.best == 2 && a2 > none;
+    const float value = two ? a1 + a2 : a1;
+    const float err = 2.f * ds + 0x1p-22f * (fabsf(a1) + (two ? fabsf(a2) : 0.f));
+    const float lo = a1 > none ? value - err : none, hi = a1 > none ? value + err : none;
+    int surely = 0, maybe = 0;                    // groups before this one
+    for (int j = 0; j < r.groups; ++j) {
+      surely += lane_f32(lo, j << r.lanes_log2) > hi;
+      maybe += !(lane_f32(hi, j << r.lanes_log2) < lo);          // itself among them
+    }
+    kept = kept && surely < r.keep;
+    doubt = kept && maybe - 1 >= r.keep && a1 > none;
+  }
+  // keys: the value's order image, its lowest bits the slot
+  uint32_t key[NPER];
+#pragma unroll
+  for (int i = 0; i < NPER; ++i)
+    key[i] = kept && c[i] > none ? (order_key(bias ? c[i] : v[i]) & ~kSlots) | (kSlots - i) : 0u;
+  sort_down(key);
+  uint32_t my_key = 0;
+  my_id = -1;
+  for (int j = 0; j <= r.k; ++j) {                // one past the last: the first that is left
+    const uint32_t best = wave_max_u32(key[0]);
+    if (best == 0u) break;
+    const bool mine = key[0] == best;
+    const int src = __ffsll((long long)__ballot(mine)) - 1;
+    const int e = __builtin_amdgcn_readlane(at.e0, src) +
+                  (int(kSlots - (best & kSlots)) << r.lanes_log2);
+    if (at.lane == j) my_key = best, my_id = e;
+    if (at.lane == src) {
+#pragma unroll
+      for (int i = 0; i + 1 < NPER; ++i) key[i] = key[i + 1];
+      key[NPER - 1] = 0u;
+    }
+  }
+  const uint32_t next = __shfl_down(my_key, 1);
+  if (at.lane < r.k && next) {
+    const uint32_t hi = my_key & ~kSlots, lo = next & ~kSlots;
+    if (bias) {
+      // 2^SB steps of the image and a rounding of the sum
+      const float x = key_value(hi), y = key_value(lo);
+      const float err = 2.f * ds + float(1u << SB) * 0x1p-22f * (fabsf(x) + fabsf(y));
+      doubt = doubt || !(x - y > err);
+    } else {
+      doubt = doubt || hi == lo;
+    }
+  }
+  if (__any(doubt)) my_id = choose_f64<NPER>(v, b, bias != nullptr, top, r, at);
+  // weights: renormalised ones are relative to the largest score, so that they
+  // hold where every s underflows
+  const bool has = at.lane < r.k && my_id >= 0;
+  const float l = row[has ? my_id : 0];
+  float p;
+  if (r.sigmoid) {
+    const float q = exp_down(-fabs(double(l)));
+    float up = l < 0.f ? q : 1.f;
+    if (r.norm) {
+      const uint32_t most = wave_max_u32(has ? order_key(l) : 0u);
+      const float lm = fminf(most ? key_value(most) : 0.f, 0.f);
+      up = l < lm ? exp_down(double(l) - double(lm)) : 1.f;
+    }
+    p = up / (1.f + q);
+  } else if (r.norm) {
+    const uint32_t most = wave_max_u32(has ? order_key(l) : 0u);
+    const float lm = key_value(most);
+    p = l == lm ? 1.f : exp_down(double(l) - double(lm));
+  } else {
+    p = (l == top ? 1.f : exp_down(double(l) - double(top))) / total;
+  }
+  p = has ? p : 0.f;
+  if (r.norm) p /= wave_sum_f32(p);
+  my_w = has ? p * r.scale : 0.f;
 }
 
 }  // namespace

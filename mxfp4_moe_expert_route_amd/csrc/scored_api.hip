@@ -16,7 +16,6 @@ constexpr int kMaxK = 32;
 constexpr int kMaxH = 16384;
 constexpr int kMaxI = 8192;
 constexpr int kMaxGroups = 64;           // one lane of a wave at least a group
-constexpr int kFusedTokens = 16;
 constexpr int kMaxLoraM = 1 << 20;
 constexpr int kMaxLoraKN = 1 << 17;
 constexpr int kMaxAdapters = 1024;       // as many as moe_permute groups by
@@ -97,7 +96,7 @@ int moe_route_scored_permute(const float* logits, const float* bias, int T, int 
     return MXM_ERR_ALIGN;
   const hipStream_t s = as_stream(stream);
   const mxm::ScoreRule r = rule(E, k, score, groups, topk_groups, group_best, renormalise, scale);
-  if (T <= kFusedTokens)
+  if (mxm::route_scored_fusable(T, r))
     return launched(mxm::launch_route_scored_permute(logits, bias, T, r, topk_ids, topk_w, counts,
                                                      offsets, sorted_pairs, pair_to_row, s));
   if (mxm::launch_route_scored(logits, bias, T, r, topk_ids, topk_w, s) != hipSuccess)
