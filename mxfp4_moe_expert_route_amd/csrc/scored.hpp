@@ -18,8 +18,9 @@
 // 32 bits tell nearly every pair of values apart, so a wave first chooses by
 // fp32 values whose error it knows, and keeps that choice if every two
 // successive values (and the last taken and the first left) are further apart
-// than their errors; otherwise it chooses again in fp64.  8192 tokens of 384
-// experts in 8 groups: 16 us, 36 in fp64 throughout.
+// than their errors. Otherwise the order of the nearest candidates is found in fp64, and
+// where that does not settle it the whole choice.  8192 tokens of 384
+// experts in 8 groups: 13 us, 36 in fp64 throughout.
 #pragma once
 #include "routing.hpp"
 
@@ -113,6 +114,35 @@ struct ScorePlace {
         e0(g * r.size + m) {}
 };
 
+__device__ __forceinline__ double lane_f64(double v, int src) {
+  const uint64_t u = uint64_t(__double_as_longlong(v));
+  const uint32_t lo = __builtin_amdgcn_readlane(int(uint32_t(u)), src);
+  const uint32_t hi = __builtin_amdgcn_readlane(int(uint32_t(u >> 32)), src);
+  return __longlong_as_double((long long)((uint64_t(hi) << 32) | lo));
+}
+
+// exp(l - top), and 1 at the top, be it infinite
+__device__ __forceinline__ double exp_f64(float l, float top) {
+  return exp(l == top ? 0.0 : double(l) - double(top));
+}
+
+__device__ __forceinline__ double score_f64(float l, float top, double total, bool sigmoid) {
+  return sigmoid ? 1.0 / (1.0 + exp(-double(l))) : exp_f64(l, top) / total;
+}
+
+// The softmax's sum; one exponential at a time, for few registers.
+template <int NPER>
+__device__ __forceinline__ double total_f64(const float (&v)[NPER], float top) {
+  double total = 0.0;
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) {
+    const double e = exp_f64(v[i], top);
+    total += v[i] > -__builtin_inff() ? e : 0.0;
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  return wave_sum_f64(total);
+}
+
 // The choice in fp64; lanes 0..k-1 end with the j-th id, or -1.  v is NaN in
 // slots without an expert, top the row's largest logit.
 template <int NPER>
@@ -121,20 +151,12 @@ __device__ __forceinline__ int choose_f64(const float (&v)[NPER], const float (&
                                           const ScorePlace& at) {
   const double none = -__builtin_inf();
   double c[NPER];                                 // -inf: not available
-  double total = 0.0;
+  double total = 1.0;
+  if (!r.sigmoid) total = total_f64<NPER>(v, top);
 #pragma unroll
   for (int i = 0; i < NPER; ++i) {
-    const double l = v[i];
-    const double s = r.sigmoid ? 1.0 / (1.0 + exp(-l)) : v[i] == top ? 1.0 : exp(l - double(top));
-    c[i] = l > none ? s : 0.0;
-    total += c[i];
-    __builtin_amdgcn_sched_barrier(0);            // one at a time: few registers
-  }
-  total = wave_sum_f64(total);
-#pragma unroll
-  for (int i = 0; i < NPER; ++i) {
-    c[i] = (r.sigmoid ? c[i] : c[i] / total) + double(b[i]);
-    if (!(double(v[i]) > none) || !(c[i] > none)) c[i] = none;
+    const double x = score_f64(v[i], top, total, r.sigmoid) + double(b[i]);
+    c[i] = double(v[i]) > none && x > none ? x : none;
     __builtin_amdgcn_sched_barrier(0);
   }
   bool kept = at.g < r.groups;
@@ -221,21 +243,31 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
   const float none = -__builtin_inff();
   const ScorePlace at(r);
   float v[NPER], b[NPER];
+  const int held = at.g < r.groups ? (r.size - at.m + at.lanes - 1) >> r.lanes_log2 : 0;
+  int place[NPER];
 #pragma unroll
   for (int i = 0; i < NPER; ++i) {
-    const bool in = at.g < r.groups && at.m + at.lanes * i < r.size;
-    v[i] = row[in ? at.e0 + at.lanes * i : 0];
-    b[i] = bias ? bias[in ? at.e0 + at.lanes * i : 0] : 0.f;
-    if (!in) v[i] = __builtin_nanf("");
+    place[i] = min(at.e0 + (i << r.lanes_log2), r.E - 1);
+    v[i] = row[place[i]];
+    b[i] = 0.f;
   }
+  if (bias) {
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) b[i] = bias[place[i]];
+  }
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) v[i] = i < held ? v[i] : __builtin_nanf("");
   // fp32 values and a bound on the scores' error
   float top = none, total = 1.f;
   if (!r.sigmoid) {
     uint32_t t = 0;
 #pragma unroll
-    for (int i = 0; i < NPER; ++i) t = max(t, v[i] > none ? order_key(v[i]) : 0u);
+    for (int i = 0; i < NPER; ++i) {
+      const uint32_t o = order_key(v[i]);         // of NaN: -inf's
+      t = max(t, o);
+    }
     t = wave_max_u32(t);
-    top = t ? key_value(t) : none;
+    top = key_value(t);
   }
   const bool scored = bias || r.groups > 1;       // else logits decide
   float c[NPER], ds = 0.f;
@@ -245,17 +277,34 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
     ds = 0x1p-21f;
 #pragma unroll
     for (int i = 0; i < NPER; ++i)
-      c[i] = scored ? __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v[i] * -1.4426950408889634f)) : 0.f;
-  } else if (scored || !r.norm) {
-    double sum = 0.0;
+      c[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v[i] * -1.4426950408889634f));
+  } else if (r.norm && scored) {
+    // with d = l - top, of exp(d): 2^-23 (|d| + 1) relative, so at most 2^-23 in
+    // all; of the sum: 2^-23 (1 + the mean of |d| by weight, at most ln E, and a
+    // quarter of its 38 additions); of each s at most 2^-23 (3 + 7 + 10) / total
+    float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NPER; ++i) {
-      c[i] = !(v[i] > none) ? 0.f : v[i] == top ? 1.f : exp_down(double(v[i]) - double(top));
+      const float d = v[i] == top ? 0.f : v[i] - top;
+      const float e = __builtin_amdgcn_exp2f(d * 1.4426950408889634f);
+      c[i] = v[i] > none ? e : 0.f;
+      sum += c[i];
+    }
+    const float inv = __builtin_amdgcn_rcpf(wave_sum_f32(sum));
+    ds = 0x1p-18f * inv;
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) c[i] *= inv;
+  } else if (!r.norm) {
+    double sum = 0.0;                             // the weights' divisor too
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+      const float e = exp_down(v[i] == top ? 0.0 : double(v[i]) - double(top));
+      c[i] = v[i] > none ? e : 0.f;
       sum += double(c[i]);
     }
     total = float(wave_sum_f64(sum));
     const float inv = __builtin_amdgcn_rcpf(total);
-    ds = 0x1p-20f * inv;                          // each s is at most 1 / total
+    ds = 0x1p-20f * inv;
 #pragma unroll
     for (int i = 0; i < NPER; ++i) c[i] *= inv;
   } else {
@@ -264,10 +313,10 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
   }
 #pragma unroll
   for (int i = 0; i < NPER; ++i) {
-    c[i] += b[i];
-    if (!(v[i] > none) || !(c[i] > none)) c[i] = none;
+    const float x = fmaxf(c[i] + b[i], none);     // NaN: none
+    c[i] = v[i] > none ? x : none;
   }
-  bool kept = at.g < r.groups, doubt = false;
+  bool kept = true, doubt = false;
   if (r.groups > 1) {
     float a1 = none, a2 = none;                   // the two largest of the group
 #pragma unroll
@@ -293,44 +342,89 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
       surely += lane_f32(lo, j << r.lanes_log2) > hi;
       maybe += !(lane_f32(hi, j << r.lanes_log2) < lo);          // itself among them
     }
-    kept = kept && surely < r.keep;
+    kept = surely < r.keep;
     doubt = kept && maybe - 1 >= r.keep && a1 > none;
   }
   // keys: the value's order image, its lowest bits the slot
   uint32_t key[NPER];
 #pragma unroll
-  for (int i = 0; i < NPER; ++i)
-    key[i] = kept && c[i] > none ? (order_key(bias ? c[i] : v[i]) & ~kSlots) | (kSlots - i) : 0u;
-  sort_down(key);
-  uint32_t my_key = 0;
-  my_id = -1;
-  for (int j = 0; j <= r.k; ++j) {                // one past the last: the first that is left
-    const uint32_t best = wave_max_u32(key[0]);
-    if (best == 0u) break;
-    const bool mine = key[0] == best;
-    const int src = __ffsll((long long)__ballot(mine)) - 1;
-    const int e = __builtin_amdgcn_readlane(at.e0, src) +
-                  (int(kSlots - (best & kSlots)) << r.lanes_log2);
-    if (at.lane == j) my_key = best, my_id = e;
-    if (at.lane == src) {
-#pragma unroll
-      for (int i = 0; i + 1 < NPER; ++i) key[i] = key[i + 1];
-      key[NPER - 1] = 0u;
-    }
+  for (int i = 0; i < NPER; ++i) {
+    // no NaN and no -0 where available
+    const uint32_t u = __float_as_uint(bias ? c[i] : v[i] + 0.f);
+    const uint32_t image = u ^ (uint32_t(int(u) >> 31) | 0x80000000u);
+    key[i] = kept && c[i] > none ? (image & ~kSlots) | (kSlots - i) : 0u;
   }
+  sort_down(key);
+  int my_key = 0, my_src = 0, found = 0;
+  bool all = false;                               // every key of the wave is taken
+  auto take = [&](int upto) {
+    while (found < upto) {
+      const uint32_t best = wave_max_u32(key[0]);
+      if (best == 0u) {
+        all = true;
+        break;
+      }
+      const int src = __ffsll((long long)__ballot(key[0] == best)) - 1;
+      if (at.lane == found) my_key = int(best), my_src = src;
+      if (at.lane == src) {
+#pragma unroll
+        for (int i = 0; i + 1 < NPER; ++i) key[i] = key[i + 1];
+        key[NPER - 1] = 0u;
+      }
+      ++found;
+    }
+  };
+  auto id_of = [&]() {
+    return !my_key ? -1
+                   : (my_src >> r.lanes_log2) * r.size + (my_src & (at.lanes - 1)) +
+                         (int(kSlots - (uint32_t(my_key) & kSlots)) << r.lanes_log2);
+  };
+  take(r.k + 1);                                  // and the first that is left
+  my_id = id_of();
+  bool close = false;
   const uint32_t next = __shfl_down(my_key, 1);
   if (at.lane < r.k && next) {
-    const uint32_t hi = my_key & ~kSlots, lo = next & ~kSlots;
+    const uint32_t hi = uint32_t(my_key) & ~kSlots, lo = next & ~kSlots;
     if (bias) {
       // 2^SB steps of the image and a rounding of the sum
       const float x = key_value(hi), y = key_value(lo);
       const float err = 2.f * ds + float(1u << SB) * 0x1p-22f * (fabsf(x) + fabsf(y));
-      doubt = doubt || !(x - y > err);
+      close = !(x - y > err);
     } else {
-      doubt = doubt || hi == lo;
+      close = hi == lo;
     }
   }
-  if (__any(doubt)) my_id = choose_f64<NPER>(v, b, bias != nullptr, top, r, at);
+  doubt = __any(doubt);
+  if (!doubt && __any(close)) {
+    // the same groups, but values too close: eight more candidates, and the
+    // candidates' order in fp64.  It stands if the k-th is above whatever is
+    // not among them.
+    take(r.k + 9);
+    my_id = id_of();
+    const float l = row[max(my_id, 0)];
+    double x = l;
+    if (bias) {
+      double sum = 1.0;
+      if (!r.sigmoid) sum = total_f64<NPER>(v, top);
+      x = score_f64(l, top, sum, r.sigmoid) + double(bias[max(my_id, 0)]);
+    }
+    int place = at.lane;                          // stays where it is: no candidate
+    if (at.lane < found) {
+      place = 0;
+      for (int j = 0; j < found; ++j) {
+        const double o = lane_f64(x, j);
+        place += o > x || (o == x && __builtin_amdgcn_readlane(my_id, j) < my_id);
+      }
+    }
+    if (!all) {
+      const float left = key_value(__builtin_amdgcn_readlane(my_key, found - 1) | kSlots);
+      const double kth = lane_f64(x, __ffsll((long long)__ballot(place == r.k - 1)) - 1);
+      const double err = bias ? double(ds) + double(float(1u << SB) * 0x1p-22f * fabsf(left)) : 0.0;
+      doubt = !(kth > double(left) + err);
+    }
+    my_id = __builtin_amdgcn_ds_permute(place << 2, my_id);
+  }
+  if (doubt) my_id = choose_f64<NPER>(v, b, bias != nullptr, top, r, at);
   // weights: renormalised ones are relative to the largest score, so that they
   // hold where every s underflows
   const bool has = at.lane < r.k && my_id >= 0;
@@ -341,8 +435,8 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
     float up = l < 0.f ? q : 1.f;
     if (r.norm) {
       const uint32_t most = wave_max_u32(has ? order_key(l) : 0u);
-      const float lm = fminf(most ? key_value(most) : 0.f, 0.f);
-      up = l < lm ? exp_down(double(l) - double(lm)) : 1.f;
+      const float lm = most ? key_value(most) : 0.f;
+      if (lm < 0.f) up = l < lm ? exp_down(double(l) - double(lm)) : 1.f;
     }
     p = up / (1.f + q);
   } else if (r.norm) {
