@@ -44,56 +44,91 @@ __device__ __forceinline__ int row_at(const LoraProblem& p, const Tile& t, int i
   return unsigned(row) < unsigned(p.M) ? row : -1;
 }
 
-// t = A_s x for a tile of 16 MS rows and one piece of K.  The workgroup's waves
-// take steps of 32 of K in turn and add up through LDS.  Of an operand lane
-// 16 g + i holds row i (of A: operand A, of x: operand B), K 8 g .. 8 g + 7; lane
-// 16 g + c of the result holds ranks 4 g .. 4 g + 3 of row c.
-template <int RP, int MS>
-__global__ __launch_bounds__(kWaves * kWave) void k_lora_shrink(LoraProblem p, int piece) {
-  constexpr int NR = (RP + 15) / 16;
-  __shared__ __attribute__((aligned(16))) float red[kWaves - 1][MS * 16][NR * 16];
-  Tile t;
-  if (!find_tile(p.offsets, p.S, 16 * MS, blockIdx.x, t)) return;
-  const int lane = lane_id(), wave = threadIdx.x >> 6;
+// acc += A_s x over the K of [k0, k1) that are a wave's: steps of 32, STRIDE apart.
+// A load takes 64 bytes of each of 16 rows by four neighbouring lanes; straight
+// in the operands' order, a row a lane, the vector cache gives less than half of
+// that rate (8.4 of 18.5 TB/s where it hits L2).  So each 1 KB block goes through
+// `stage`, (MS + NR) KB of LDS that no other wave touches: piece q of row i at
+// 256 q + 16 (i ^ 4 q), which both sides reach without bank conflicts.  Of an
+// operand lane 16 g + i holds row i (of A: operand A, of x: operand B), K 8 g ..
+// 8 g + 7; lane 16 g + c of the result holds ranks 4 g .. 4 g + 3 of row c.  Rows
+// past the tile and ranks past the last repeat others and are not used.
+template <int NR, int MS>
+__device__ __forceinline__ void shrink_part(const LoraProblem& p, const Tile& t, int k0, int k1,
+                                            int stride, char* stage, f32x4 (&acc)[MS][NR]) {
+  constexpr int R = MS + NR;
+  constexpr int U = R <= 2 ? 6 : R <= 3 ? 4 : R <= 5 ? 3 : 2;     // steps whose loads go out together
+  const int lane = lane_id();
+  const int lr = lane >> 2, lp = lane & 3;       // loading: row and piece
   const int c = lane & 15, g = lane >> 4;
-  const uint16_t* xr[MS];
+  const uint16_t* src[R];
 #pragma unroll
-  for (int m = 0; m < MS; ++m) xr[m] = p.x + size_t(max(row_at(p, t, 16 * m + c), 0)) * p.K + 8 * g;
-  const uint16_t* ar[NR];
+  for (int m = 0; m < MS; ++m)
+    src[m] = p.x + size_t(max(row_at(p, t, 16 * m + lr), 0)) * p.K;
 #pragma unroll
   for (int j = 0; j < NR; ++j)
-    ar[j] = p.a + (size_t(t.e) * p.r + min(16 * j + c, p.r - 1)) * p.K + 8 * g;
-  f32x4 acc[MS][NR];
+    src[MS + j] = p.a + (size_t(t.e) * p.r + min(16 * j + lr, p.r - 1)) * p.K;
+  char* put = stage + 256 * lp + 16 * (lr ^ (4 * lp));
+  const char* get = stage + 256 * g + 16 * (c ^ (4 * g));
+  for (int k = k0; k < k1; k += stride * U) {
+    uint4 v[U][R];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = k + stride * u + 8 * lp;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        v[u][i] = *reinterpret_cast<const uint4*>(src[i] + (at < k1 ? at : 0));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k + stride * u >= k1) break;           // wave-uniform
+      const bool in = k + stride * u + 8 * lp < k1;
+      uint4 o[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        *reinterpret_cast<uint4*>(put + 1024 * i) = in ? v[u][i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < R; ++i) o[i] = *reinterpret_cast<const uint4*>(get + 1024 * i);
+#pragma unroll
+      for (int j = 0; j < NR; ++j)
+#pragma unroll
+        for (int m = 0; m < MS; ++m) acc[m][j] = mfma(o[MS + j], o[m], acc[m][j]);
+    }
+  }
+}
+
+template <int NR, int MS>
+__device__ __forceinline__ void clear(f32x4 (&acc)[MS][NR]) {
 #pragma unroll
   for (int m = 0; m < MS; ++m)
 #pragma unroll
     for (int j = 0; j < NR; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int k1 = min(p.K, int(blockIdx.y + 1) * piece);
-  for (int k = blockIdx.y * piece + 32 * wave; k < k1; k += 32 * kWaves) {
-    const bool in = k + 8 * g < k1;
-    const int kk = in ? k : 0;
-    uint4 xv[MS], av[NR];
-#pragma unroll
-    for (int m = 0; m < MS; ++m) {
-      const uint4 v = *reinterpret_cast<const uint4*>(xr[m] + (in ? kk : -8 * g));
-      xv[m] = in ? v : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int j = 0; j < NR; ++j) {
-      const uint4 v = *reinterpret_cast<const uint4*>(ar[j] + (in ? kk : -8 * g));
-      av[j] = in && 16 * j + c < p.r ? v : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int m = 0; m < MS; ++m)
-#pragma unroll
-      for (int j = 0; j < NR; ++j) acc[m][j] = mfma(av[j], xv[m], acc[m][j]);
-  }
+}
+
+// t = A_s x for a tile of 16 MS rows and one piece of K, into `part`.  The
+// workgroup's waves take steps in turn and add up through LDS.
+template <int RP, int MS>
+__global__ __launch_bounds__(kWaves * kWave) void k_lora_shrink(LoraProblem p, int piece) {
+  constexpr int NR = (RP + 15) / 16;
+  constexpr int kStage = (MS + NR) * 1024, kRed = MS * NR * 1024;
+  constexpr int kBytes = kWaves * kStage > (kWaves - 1) * kRed ? kWaves * kStage : (kWaves - 1) * kRed;
+  __shared__ __attribute__((aligned(16))) char lds[kBytes];
+  Tile t;
+  if (!find_tile(p.offsets, p.S, 16 * MS, blockIdx.x, t)) return;
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  const int c = lane & 15, g = lane >> 4;
+  f32x4 acc[MS][NR];
+  clear(acc);
+  shrink_part(p, t, blockIdx.y * piece + 32 * wave, min(p.K, int(blockIdx.y + 1) * piece),
+              32 * kWaves, lds + wave * kStage, acc);
+  __syncthreads();                               // `red` lies where the stages were
+  f32x4* red = reinterpret_cast<f32x4*>(lds);
   if (wave > 0) {
 #pragma unroll
     for (int m = 0; m < MS; ++m)
 #pragma unroll
-      for (int j = 0; j < NR; ++j)
-        *reinterpret_cast<f32x4*>(&red[wave - 1][16 * m + c][16 * j + 4 * g]) = acc[m][j];
+      for (int j = 0; j < NR; ++j) red[((wave - 1) * MS * NR + m * NR + j) * kWave + lane] = acc[m][j];
   }
   __syncthreads();
   if (wave > 0) return;
@@ -106,8 +141,7 @@ __global__ __launch_bounds__(kWaves * kWave) void k_lora_shrink(LoraProblem p, i
     for (int j = 0; j < NR; ++j) {
       f32x4 v = acc[m][j];
 #pragma unroll
-      for (int w = 0; w < kWaves - 1; ++w)
-        v += *reinterpret_cast<const f32x4*>(&red[w][i][16 * j + 4 * g]);
+      for (int w = 0; w < kWaves - 1; ++w) v += red[(w * MS * NR + m * NR + j) * kWave + lane];
       if (ok && 16 * j + 4 * g < RP)
         *reinterpret_cast<f32x4*>(p.part + (size_t(blockIdx.y) * p.M + pos) * RP + 16 * j + 4 * g) = v;
     }
@@ -117,148 +151,377 @@ __global__ __launch_bounds__(kWaves * kWave) void k_lora_shrink(LoraProblem p, i
 // Eight elements of row n of B from rank 8 q on; 0 past the rank.
 template <bool VEC>
 __device__ __forceinline__ uint4 load_b(const uint16_t* row, int q, int r) {
-  uint4 v = make_uint4(0, 0, 0, 0);
   if constexpr (VEC) {
-    if (8 * q < r) v = *reinterpret_cast<const uint4*>(row + 8 * q);
+    const uint4 v = *reinterpret_cast<const uint4*>(row + (8 * q < r ? 8 * q : 0));
+    return 8 * q < r ? v : make_uint4(0, 0, 0, 0);
   } else {
     uint32_t h[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = 8 * q + i < r ? row[8 * q + i] : 0;
-    v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t v = row[min(8 * q + i, r - 1)];
+      h[i] = 8 * q + i < r ? v : 0;
+    }
+    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+  }
+}
+
+// Four neighbouring elements of y, as fp32.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ f32x4 load_y(const void* y, size_t at, int n, int N) {
+  f32x4 v;
+  if constexpr (BF16) {
+    const uint16_t* q = static_cast<const uint16_t*>(y) + at;
+    uint2 u = make_uint2(0, 0);
+    if constexpr (VEC) {
+      if (n < N) u = *reinterpret_cast<const uint2*>(q);
+    } else {
+      if (n < N) u.x = q[0];
+      if (n + 1 < N) u.x |= uint32_t(q[1]) << 16;
+      if (n + 2 < N) u.y = q[2];
+      if (n + 3 < N) u.y |= uint32_t(q[3]) << 16;
+    }
+    v[0] = __uint_as_float(u.x << 16);
+    v[1] = __uint_as_float(u.x & 0xffff0000u);
+    v[2] = __uint_as_float(u.y << 16);
+    v[3] = __uint_as_float(u.y & 0xffff0000u);
+  } else {
+    const float* q = static_cast<const float*>(y) + at;
+    v = f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (VEC) {
+      if (n < N) v = *reinterpret_cast<const f32x4*>(q);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < N) v[i] = q[i];
+    }
   }
   return v;
+}
+
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void store_y(void* y, size_t at, int n, int N, f32x4 v) {
+  if constexpr (BF16) {
+    uint16_t* q = static_cast<uint16_t*>(y) + at;
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = f32_to_bf16_rne(v[i]);
+    if constexpr (VEC) {
+      if (n < N) *reinterpret_cast<uint2*>(q) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < N) q[i] = uint16_t(h[i]);
+    }
+  } else {
+    float* q = static_cast<float*>(y) + at;
+    if constexpr (VEC) {
+      if (n < N) *reinterpret_cast<f32x4*>(q) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < N) q[i] = v[i];
+    }
+  }
 }
 
 // y += scale B_s t for a tile of 16 MS rows and 64 columns a wave.  t is fp32
 // and B bf16: t is cut into three bf16 of 8 bits each by truncation, which is
 // exact, and the three meet the same B along the instruction's K: octet q of K
 // is octet q % (RP / 8) of the rank in part q / (RP / 8).  Product j of four
-// takes the columns 16 (i / 4) + 4 j + i % 4 as its rows i, so lane 16 g + c ends
-// with the 16 columns from 16 g on of row c.
-template <int RP, int MS, bool BF16, bool VECB, bool VECY>
-__global__ __launch_bounds__(kWaves * kWave) void k_lora_expand(LoraProblem p, int splits) {
-  constexpr int OCT = RP / 8, NM = (3 * OCT + 3) / 4;
-  constexpr int LD = 32 * NM + 8;                // bf16 a row in LDS
-  __shared__ __attribute__((aligned(16))) uint16_t ts[MS * 16][LD];
-  Tile t;
-  if (!find_tile(p.offsets, p.S, 16 * MS, blockIdx.x, t)) return;
-  const int lane = lane_id(), wave = threadIdx.x >> 6;
-  const int c = lane & 15, g = lane >> 4;
-  const float scale = p.scale ? p.scale[t.e] : 1.f;
-  for (int i = threadIdx.x; i < MS * 16 * RP; i += kWaves * kWave) {
-    const int row = i / RP, j = i % RP, pos = t.row0 + row;
-    float v = 0.f;
-    // past the rank an infinite x times the padding's 0 is NaN
-    if (j < p.r && row < t.rows && unsigned(pos) < unsigned(p.M))
-      for (int s = 0; s < splits; ++s) v += p.part[(size_t(s) * p.M + pos) * RP + j];
-    v *= scale;
-    const uint32_t hi = __float_as_uint(v) & 0xffff0000u;
+// takes the columns 4 c + j, so lane 16 g + c ends with the four columns from
+// 4 c on of the rows 4 g .. 4 g + 3, and a load or store of y covers whole
+// pieces of 64 columns.
+template <int RP>
+struct Parts {
+  static constexpr int OCT = RP / 8, NM = (3 * OCT + 3) / 4;
+  static constexpr int NB = RP >= 32 ? RP / 32 : NM;     // different operands of B among the NM
+  static constexpr int LD = 32 * NM + 8;                 // bf16 a row in LDS
+};
+
+// Ranks j .. j + 3 of a row of t, in three parts.
+template <int RP>
+__device__ __forceinline__ void put_t(uint16_t* row, int j, int r, float scale, f32x4 v) {
+  uint32_t part[3][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // past the rank: not t's, and an infinite x times 0 is NaN
+    const float f = j + i < r ? v[i] * scale : 0.f;
+    const uint32_t hi = __float_as_uint(f) & 0xffff0000u;
     // an infinite or NaN t has no parts below
     const bool fin = (hi & 0x7f800000u) != 0x7f800000u;
-    const float rest = fin ? v - __uint_as_float(hi) : 0.f;
+    const float rest = fin ? f - __uint_as_float(hi) : 0.f;
     const uint32_t mid = __float_as_uint(rest) & 0xffff0000u;
-    const float low = rest - __uint_as_float(mid);
-    ts[row][j] = uint16_t(hi >> 16);
-    ts[row][RP + j] = uint16_t(mid >> 16);
-    ts[row][2 * RP + j] = uint16_t(__float_as_uint(low) >> 16);
+    part[0][i] = hi;
+    part[1][i] = mid;
+    part[2][i] = __float_as_uint(rest - __uint_as_float(mid));
   }
-  if constexpr (3 * RP < 32 * NM) {
-    for (int i = threadIdx.x; i < MS * 16 * (32 * NM - 3 * RP); i += kWaves * kWave)
-      ts[i / (32 * NM - 3 * RP)][3 * RP + i % (32 * NM - 3 * RP)] = 0;
-  }
-  __syncthreads();
-  int row[MS];
 #pragma unroll
-  for (int m = 0; m < MS; ++m) row[m] = row_at(p, t, 16 * m + c);
-  for (int n0 = (blockIdx.y * kWaves + wave) * kCols; n0 < p.N; n0 += gridDim.y * kWaves * kCols) {
-    f32x4 acc[MS][4];
+  for (int s = 0; s < 3; ++s)
+    *reinterpret_cast<uint2*>(row + s * RP + j) =
+        make_uint2(part[s][0] >> 16 | (part[s][1] & 0xffff0000u), part[s][2] >> 16 | (part[s][3] & 0xffff0000u));
+}
+
+// the rest of a row of `ts`, up to the instruction's K
+template <int RP, int MS>
+__device__ __forceinline__ void clear_tail(uint16_t* ts, int tid, int threads) {
+  using P = Parts<RP>;
+  constexpr int kTail = 32 * P::NM - 3 * RP;
+  if constexpr (kTail > 0)
+    for (int i = tid; i < MS * 16 * kTail; i += threads) ts[i / kTail * P::LD + 3 * RP + i % kTail] = 0;
+}
+
+template <int RP, bool VECB>
+__device__ __forceinline__ void load_bv(const LoraProblem& p, const Tile& t, int n0,
+                                        uint4 (&bv)[Parts<RP>::NB][4]) {
+  using P = Parts<RP>;
+  const int lane = lane_id(), c = lane & 15, g = lane >> 4;
 #pragma unroll
-    for (int m = 0; m < MS; ++m)
+  for (int j = 0; j < 4; ++j) {
+    const int n = min(n0 + 4 * c + j, p.N - 1);
+    const uint16_t* br = p.b + (size_t(t.e) * p.N + n) * p.r;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = min(n0 + 16 * (c >> 2) + 4 * j + (c & 3), p.N - 1);
-      const uint16_t* br = p.b + (size_t(t.e) * p.N + n) * p.r;
-#pragma unroll
-      for (int q = 0; q < NM; ++q) {
-        const int oct = 4 * q + g;
-        const uint4 bv = oct < 3 * OCT ? load_b<VECB>(br, oct % OCT, p.r) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int m = 0; m < MS; ++m)
-          acc[m][j] = mfma(bv, *reinterpret_cast<const uint4*>(&ts[16 * m + c][32 * q + 8 * g]), acc[m][j]);
-      }
-    }
-#pragma unroll
-    for (int m = 0; m < MS; ++m) {
-      if (row[m] < 0) continue;
-      const int n = n0 + 16 * g;
-      if constexpr (BF16) {
-        uint16_t* y = static_cast<uint16_t*>(p.y) + size_t(row[m]) * p.N + n;
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-          const float d[8] = {acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3],
-                              acc[m][j + 1][0], acc[m][j + 1][1], acc[m][j + 1][2], acc[m][j + 1][3]};
-          if (VECY) {
-            if (n + 4 * j >= p.N) continue;
-            uint4 v = *reinterpret_cast<const uint4*>(y + 4 * j);
-            uint32_t* u = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              u[q] = f32_to_bf16_rne(__uint_as_float(u[q] << 16) + d[2 * q]) |
-                     f32_to_bf16_rne(__uint_as_float(u[q] & 0xffff0000u) + d[2 * q + 1]) << 16;
-            *reinterpret_cast<uint4*>(y + 4 * j) = v;
-          } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              if (n + 4 * j + q < p.N)
-                y[4 * j + q] = uint16_t(f32_to_bf16_rne(__uint_as_float(uint32_t(y[4 * j + q]) << 16) + d[q]));
-          }
-        }
-      } else {
-        float* y = static_cast<float*>(p.y) + size_t(row[m]) * p.N + n;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (VECY) {
-            if (n + 4 * j < p.N) *reinterpret_cast<f32x4*>(y + 4 * j) += acc[m][j];
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (n + 4 * j + q < p.N) y[4 * j + q] += acc[m][j][q];
-          }
-        }
-      }
+    for (int q = 0; q < P::NB; ++q) {
+      const int oct = 4 * q + g;
+      bv[q][j] = load_b<VECB>(br, oct % P::OCT, p.r);
+      if (oct >= 3 * P::OCT) bv[q][j] = make_uint4(0, 0, 0, 0);
     }
   }
 }
 
+// columns n0 .. n0 + 63 of the tile
+template <int RP, int MS, bool BF16, bool VECY>
+__device__ __forceinline__ void expand_cols(const LoraProblem& p, const uint16_t* ts, int n0,
+                                            const int (&row)[MS][4],
+                                            const uint4 (&bv)[Parts<RP>::NB][4]) {
+  using P = Parts<RP>;
+  const int lane = lane_id(), c = lane & 15, g = lane >> 4;
+  const int n = n0 + 4 * c;
+  constexpr int G = MS > 1 && VECY ? 2 : 1;      // row tiles whose y is in flight together
+#pragma unroll
+  for (int m0 = 0; m0 < MS; m0 += G) {
+    f32x4 yv[G][4];
+#pragma unroll
+    for (int m = 0; m < G; ++m)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int at = row[m0 + m][q];
+        yv[m][q] = load_y<BF16, VECY>(p.y, size_t(max(at, 0)) * p.N + n, at < 0 ? p.N : n, p.N);
+      }
+#pragma unroll
+    for (int m = 0; m < G; ++m) {
+      f32x4 acc[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < P::NM; ++q) {
+        const uint4 tv = *reinterpret_cast<const uint4*>(ts + (16 * (m0 + m) + c) * P::LD + 32 * q + 8 * g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = mfma(tv, bv[q % P::NB][j], acc[j]);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int at = row[m0 + m][q];
+        const f32x4 d = {acc[0][q], acc[1][q], acc[2][q], acc[3][q]};
+        if (at >= 0) store_y<BF16, VECY>(p.y, size_t(at) * p.N + n, n, p.N, yv[m][q] + d);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+template <int MS>
+__device__ __forceinline__ void rows_of(const LoraProblem& p, const Tile& t, int (&row)[MS][4]) {
+  const int g = lane_id() >> 4;
+#pragma unroll
+  for (int m = 0; m < MS; ++m)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) row[m][q] = row_at(p, t, 16 * m + 4 * g + q);
+}
+
+template <int RP, int MS, bool BF16, bool VECB, bool VECY>
+__global__ __launch_bounds__(kWaves * kWave) void k_lora_expand(LoraProblem p, int splits) {
+  using P = Parts<RP>;
+  constexpr int kThreads = kWaves * kWave;
+  constexpr int kItems = MS * 16 * RP / 4;               // four ranks of a row
+  constexpr int kEach = (kItems + kThreads - 1) / kThreads;
+  __shared__ __attribute__((aligned(16))) uint16_t ts[MS * 16 * P::LD];
+  Tile t;
+  if (!find_tile(p.offsets, p.S, 16 * MS, blockIdx.x, t)) return;
+  const int wave = threadIdx.x >> 6;
+  const int step = gridDim.y * kWaves * kCols;
+  int n0 = (blockIdx.y * kWaves + wave) * kCols;
+  uint4 bv[P::NB][4];
+  if (n0 < p.N) load_bv<RP, VECB>(p, t, n0, bv);
+  const float scale = p.scale ? p.scale[t.e] : 1.f;
+  const float* src[kEach];
+  f32x4 sum[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int it = threadIdx.x + kThreads * i, row = it / (RP / 4), pos = t.row0 + row;
+    const bool ok = row < t.rows && unsigned(pos) < unsigned(p.M);
+    src[i] = p.part + size_t(ok ? pos : 0) * RP + 4 * (it % (RP / 4));
+    sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  for (int s0 = 0; s0 < splits; s0 += 4) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool in = s0 + u < splits;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const f32x4 w = *reinterpret_cast<const f32x4*>(src[i] + size_t(in ? s0 + u : 0) * p.M * RP);
+        sum[i] += in ? w : f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int it = threadIdx.x + kThreads * i;
+    if (it < kItems) put_t<RP>(ts + it / (RP / 4) * P::LD, 4 * (it % (RP / 4)), p.r, scale, sum[i]);
+  }
+  clear_tail<RP, MS>(ts, threadIdx.x, kThreads);
+  int row[MS][4];
+  rows_of(p, t, row);
+  __syncthreads();
+  while (n0 < p.N) {
+    expand_cols<RP, MS, BF16, VECY>(p, ts, n0, row, bv);
+    n0 += step;
+    if (n0 < p.N) load_bv<RP, VECB>(p, t, n0, bv);
+  }
+}
+
+// Both steps of a tile in one workgroup of 16 waves, which computes t for itself:
+// one launch, no workspace, and t once for each of gridDim.y column ranges.
+constexpr int kFusedWaves = 16;
+
 template <int RP, int MS>
-hipError_t launch(const LoraProblem& p, hipStream_t s) {
+struct FusedLds {
+  static constexpr int NR = (RP + 15) / 16;
+  static constexpr int kStage = (MS + NR) * 1024, kRed = MS * NR * 1024;
+  static constexpr int kWork = kFusedWaves * (kStage > kRed ? kStage : kRed);
+  static constexpr int kBytes = kWork + MS * 16 * Parts<RP>::LD * 2;
+};
+
+template <int RP, int MS, bool BF16, bool VECB, bool VECY>
+__global__ __launch_bounds__(kFusedWaves * kWave) void k_lora_fused(LoraProblem p, int chunks) {
+  using P = Parts<RP>;
+  using L = FusedLds<RP, MS>;
+  constexpr int NR = L::NR;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  uint16_t* ts = reinterpret_cast<uint16_t*>(smem + L::kWork);
+  Tile t;
+  if (!find_tile(p.offsets, p.S, 16 * MS, blockIdx.x, t)) return;
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  // column pieces blockIdx.y * chunks + wave, + 16, ...
+  const int n1 = min(p.N, int(blockIdx.y + 1) * chunks * kCols);
+  int n0 = (blockIdx.y * chunks + wave) * kCols;
+  uint4 bv[P::NB][4];
+  constexpr bool kEarly = P::NB * 4 + MS * NR <= 8;      // registers for B throughout
+  if (kEarly && n0 < n1) load_bv<RP, VECB>(p, t, n0, bv);
+  const float scale = p.scale ? p.scale[t.e] : 1.f;
+  f32x4 acc[MS][NR];
+  clear(acc);
+  shrink_part(p, t, 32 * wave, p.K, 32 * kFusedWaves, smem + wave * L::kStage, acc);
+  if (!kEarly && n0 < n1) load_bv<RP, VECB>(p, t, n0, bv);
+  __syncthreads();                               // `red` lies where the stages were
+  f32x4* red = reinterpret_cast<f32x4*>(smem);
+#pragma unroll
+  for (int m = 0; m < MS; ++m)
+#pragma unroll
+    for (int j = 0; j < NR; ++j) red[(wave * MS * NR + m * NR + j) * kWave + lane] = acc[m][j];
+  clear_tail<RP, MS>(ts, threadIdx.x, kFusedWaves * kWave);
+  int row[MS][4];
+  rows_of(p, t, row);
+  __syncthreads();
+  // item (m, j, lane) as the waves hold it: ranks 16 j + 4 g .. + 3 of row 16 m + c
+  for (int it = threadIdx.x; it < MS * NR * kWave; it += kFusedWaves * kWave) {
+    f32x4 v = red[it];
+#pragma unroll
+    for (int w = 1; w < kFusedWaves; ++w) v += red[w * MS * NR * kWave + it];
+    const int mj = it / kWave, l = it % kWave;
+    const int j = 16 * (mj % NR) + 4 * (l >> 4);
+    if (j < RP) put_t<RP>(ts + (16 * (mj / NR) + (l & 15)) * P::LD, j, p.r, scale, v);
+  }
+  __syncthreads();
+  while (n0 < n1) {
+    expand_cols<RP, MS, BF16, VECY>(p, ts, n0, row, bv);
+    n0 += kFusedWaves * kCols;
+    if (n0 < n1) load_bv<RP, VECB>(p, t, n0, bv);
+  }
+}
+
+// f(bf16, vector loads of B, vector accesses of y), as types
+template <class F>
+void by_form(const LoraProblem& p, F f) {
+  const int es = p.bf16 ? 2 : 4;
+  const bool vb = p.r % 8 == 0;
+  const bool vy = p.N % 4 == 0 && reinterpret_cast<uintptr_t>(p.y) % (4 * es) == 0;
+  const std::true_type yes;
+  const std::false_type no;
+  if (p.bf16) {
+    if (vb) { if (vy) f(yes, yes, yes); else f(yes, yes, no); }
+    else { if (vy) f(yes, no, yes); else f(yes, no, no); }
+  } else {
+    if (vb) { if (vy) f(no, yes, yes); else f(no, yes, no); }
+    else { if (vy) f(no, no, yes); else f(no, no, no); }
+  }
+}
+
+template <int RP, int MS>
+hipError_t launch_two(const LoraProblem& p, hipStream_t s) {
   const unsigned tiles = unsigned(most_tiles(p, 16 * MS));
   const int splits = k_splits(p);
   const int unit = 32 * kWaves;
   const int piece = ((p.K + splits - 1) / splits + unit - 1) / unit * unit;
   k_lora_shrink<RP, MS><<<dim3(tiles, splits), kWaves * kWave, 0, s>>>(p, piece);
-  // a launch has fewer than 2^32 threads: workgroups go on to further columns
+  // enough workgroups for the chip, and no more: each sums its rows' pieces first
   const unsigned cols = unsigned((p.N + kWaves * kCols - 1) / (kWaves * kCols));
-  const unsigned most = (1u << 23) / tiles;
+  const unsigned most = 512 / tiles + 1;
   const dim3 grid(tiles, cols < most ? cols : most);
-  const bool vb = p.r % 8 == 0;
-  const bool vy = (p.N * (p.bf16 ? 2 : 4)) % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0;
-  auto go = [&](auto bf, auto vecb, auto vecy) {
+  by_form(p, [&](auto bf, auto vecb, auto vecy) {
     k_lora_expand<RP, MS, decltype(bf)::value, decltype(vecb)::value, decltype(vecy)::value>
         <<<grid, kWaves * kWave, 0, s>>>(p, splits);
-  };
-  const std::true_type yes;
-  const std::false_type no;
-  if (p.bf16) {
-    if (vb) { if (vy) go(yes, yes, yes); else go(yes, yes, no); }
-    else { if (vy) go(yes, no, yes); else go(yes, no, no); }
-  } else {
-    if (vb) { if (vy) go(no, yes, yes); else go(no, yes, no); }
-    else { if (vy) go(no, no, yes); else go(no, no, no); }
-  }
+  });
   return hipGetLastError();
+}
+
+template <int RP, int MS>
+hipError_t launch_fused(const LoraProblem& p, hipStream_t s) {
+  const unsigned tiles = unsigned(most_tiles(p, 16 * MS));
+  const unsigned cols = unsigned((p.N + kCols - 1) / kCols);
+  unsigned ranges = (255 + tiles) / tiles;
+  ranges = ranges < cols ? ranges : cols;
+  const int chunks = int((cols + ranges - 1) / ranges);
+  const dim3 grid(tiles, (cols + chunks - 1) / chunks);
+  hipError_t e = hipSuccess;
+  by_form(p, [&](auto bf, auto vecb, auto vecy) {
+    const auto fn = &k_lora_fused<RP, MS, decltype(bf)::value, decltype(vecb)::value, decltype(vecy)::value>;
+    constexpr int lds = FusedLds<RP, MS>::kBytes;
+    if (lds > 64 * 1024) {
+      static std::atomic<bool> set[kMaxDevices];
+      e = lds_limit_once(reinterpret_cast<const void*>(fn), lds, set);
+      if (e != hipSuccess) return;
+    }
+    fn<<<grid, kFusedWaves * kWave, lds, s>>>(p, chunks);
+  });
+  return e != hipSuccess ? e : hipGetLastError();
+}
+
+#ifndef LORA_FORCE
+#define LORA_FORCE 0
+#endif
+bool fused(const LoraProblem& p) {
+  if (LORA_FORCE == 1) return p.r <= 64 && tile_rows(p) * ((padded(p.r) + 15) / 16) <= 8;
+  if (LORA_FORCE == 2) return false;
+  const int ms = tile_rows(p), nr = (padded(p.r) + 15) / 16;
+  return p.r <= 64 && ms * nr <= 8 && int64_t(ms + nr) * 32 * p.K <= 512 * 1024;
+}
+
+template <int RP, int MS>
+hipError_t launch(const LoraProblem& p, hipStream_t s) {
+  if constexpr (RP <= 64 && MS * ((RP + 15) / 16) <= 8) {
+    if (fused(p)) return launch_fused<RP, MS>(p, s);
+  }
+  return launch_two<RP, MS>(p, s);
 }
 
 template <int RP>
@@ -274,7 +537,7 @@ hipError_t launch_r(const LoraProblem& p, hipStream_t s) {
 size_t lora_workspace_bytes(int M, int K, int N, int S, int r) {
   LoraProblem p{};
   p.M = M; p.K = K; p.N = N; p.S = S; p.r = r;
-  return size_t(k_splits(p)) * M * padded(r) * sizeof(float);
+  return fused(p) ? 0 : size_t(k_splits(p)) * M * padded(r) * sizeof(float);
 }
 
 hipError_t launch_lora(const LoraProblem& p, hipStream_t s) {

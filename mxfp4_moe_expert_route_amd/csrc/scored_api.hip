@@ -159,8 +159,9 @@ int lora_add(const uint16_t* x_bf16, const int32_t* sorted_rows, const int32_t* 
   if (y_dtype != MXM_F32 && y_dtype != MXM_BF16) return MXM_ERR_DTYPE;
   if (!lora_shape(M, K, N, S, r)) return MXM_ERR_SHAPE;
   if (M == 0 || N == 0) return MXM_OK;
-  if (workspace_bytes < mxm::lora_workspace_bytes(M, K, N, S, r)) return MXM_ERR_WORKSPACE;
-  if (!x_bf16 || !sorted_rows || !offsets || !a_bf16 || !b_bf16 || !y || !workspace)
+  const size_t need = mxm::lora_workspace_bytes(M, K, N, S, r);
+  if (workspace_bytes < need) return MXM_ERR_WORKSPACE;
+  if (!x_bf16 || !sorted_rows || !offsets || !a_bf16 || !b_bf16 || !y || (need > 0 && !workspace))
     return MXM_ERR_NULL;
   if (!aligned(x_bf16, 16) || !aligned(a_bf16, 16) || !aligned(b_bf16, 16) ||
       !aligned(workspace, 16) || !aligned(sorted_rows, 4) || !aligned(offsets, 4) ||

@@ -91,7 +91,7 @@ def test_layer_argument_checks(lib):
 
 def test_lora_argument_checks(lib):
     f = lib.lora_add         # x, rows, offsets, M, K, N, S, r, a, b, scale, y, dtype, ws, bytes, stream
-    shape = (8, 64, 100, 4, 16)
+    shape = (8, 64, 100, 4, 100)          # sizes that need a workspace
     need = lib.lora_add_workspace_bytes(*shape)
     assert need > 0
     ok = dict(p=[P] * 3, shape=shape, q=[P] * 4, dtype=1, ws=P, n=1 << 62)
@@ -125,6 +125,7 @@ def test_lora_argument_checks(lib):
     assert call(shape=(0, 64, 100, 4, 16), p=[None] * 3, q=[None] * 4, ws=None, n=0) == 0
     assert call(shape=(8, 64, 0, 4, 16), p=[None] * 3, q=[None] * 4, ws=None, n=0) == 0
     assert lib.lora_add_workspace_bytes(0, 64, 100, 4, 16) == 0
+    assert lib.lora_add_workspace_bytes(8, 64, 100, 4, 16) == 0          # one launch: none needed
 
 
 def test_wrappers_refuse_host_tensors_and_wrong_types():

@@ -175,7 +175,7 @@ def test_adapters_of_other_rows_do_not_leak(mm):
 def test_workspace_streams_replays_and_refusals(mm):
     say("lora_add buffers, streams, replays")
     rng = np.random.default_rng(7)
-    for M, K, N, S, r in ((8, 512, 100, 2, 8), (200, 256, 130, 5, 24)):
+    for M, K, N, S, r in ((8, 512, 100, 2, 8), (200, 256, 130, 5, 24), (40, 264, 72, 3, 100)):
         x, a, b, y, scale = inputs(rng, M, K, N, S, r, False)
         (xt, _), (at, _), (bt, _), (yt, _) = bf16(x), bf16(a), bf16(b), store(y, torch.float32)
         sc = torch.from_numpy(scale.astype(np.float32)).to(DEV)
@@ -204,7 +204,7 @@ def test_workspace_streams_replays_and_refusals(mm):
             torch.cuda.synchronize()
             assert torch.equal(out, want[i % 3]), i
     with pytest.raises(mm._lib.MxmError):
-        mm.lora_add(xt, *sets[0], at, bt, yt, workspace=ws[:16])
+        mm.lora_add(xt, *sets[0], at, bt, yt, workspace=ws[:-1])
     with pytest.raises(ValueError):
         mm.lora_add(xt, *sets[0], at, bt[:, :, :8], yt)
     with pytest.raises(ValueError):
