@@ -8,15 +8,22 @@
 namespace mxm {
 namespace {
 
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef __attribute__((ext_vector_type(4))) int i32x4;
+
 constexpr int kWaves = 4;
 constexpr int kCols = 64;            // columns of y a wave holds at a time
 
 // rank padded to a size that the kernels are made for
 int padded(int r) { return r <= 8 ? 8 : r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 
+#ifndef LORA_FORCE
+#define LORA_FORCE 0
+#endif
+// row tiles of 16 a workgroup takes: two where that leaves a workgroup for every CU
 int tile_rows(const LoraProblem& p) {
   const int mean = p.M / (p.M < p.S ? p.M : p.S);
-  return mean <= 16 ? 1 : mean <= 32 || p.r > 64 ? 2 : 4;
+  return mean >= 32 && p.M >= 4096 ? 2 : 1;
 }
 
 int64_t most_tiles(const LoraProblem& p, int mt) {
@@ -148,55 +155,35 @@ __global__ __launch_bounds__(kWaves * kWave) void k_lora_shrink(LoraProblem p, i
   }
 }
 
-// Eight elements of row n of B from rank 8 q on; 0 past the rank.
-template <bool VEC>
-__device__ __forceinline__ uint4 load_b(const uint16_t* row, int q, int r) {
+// Four neighbouring elements of y as they lie in memory.
+template <bool BF16>
+using RawY = std::conditional_t<BF16, uint2, f32x4>;
+
+// columns past the last repeat it, and are not stored
+template <bool BF16, bool VEC>
+__device__ __forceinline__ RawY<BF16> load_y(const void* y, size_t at, int n, int N) {
   if constexpr (VEC) {
-    const uint4 v = *reinterpret_cast<const uint4*>(row + (8 * q < r ? 8 * q : 0));
-    return 8 * q < r ? v : make_uint4(0, 0, 0, 0);
-  } else {
-    uint32_t h[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t v = row[min(8 * q + i, r - 1)];
-      h[i] = 8 * q + i < r ? v : 0;
+    n = min(n, N - 4);                           // N is a multiple of 4
+    if constexpr (BF16) {
+      return *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(y) + at + n);
+    } else {
+      return *reinterpret_cast<const f32x4*>(static_cast<const float*>(y) + at + n);
     }
-    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+  } else if constexpr (BF16) {
+    const uint16_t* q = static_cast<const uint16_t*>(y) + at;
+    const uint32_t v0 = q[min(n, N - 1)], v1 = q[min(n + 1, N - 1)], v2 = q[min(n + 2, N - 1)], v3 = q[min(n + 3, N - 1)];
+    return make_uint2(v0 | v1 << 16, v2 | v3 << 16);
+  } else {
+    const float* q = static_cast<const float*>(y) + at;
+    return f32x4{q[min(n, N - 1)], q[min(n + 1, N - 1)], q[min(n + 2, N - 1)], q[min(n + 3, N - 1)]};
   }
 }
 
-// Four neighbouring elements of y, as fp32.
-template <bool BF16, bool VEC>
-__device__ __forceinline__ f32x4 load_y(const void* y, size_t at, int n, int N) {
-  f32x4 v;
-  if constexpr (BF16) {
-    const uint16_t* q = static_cast<const uint16_t*>(y) + at;
-    uint2 u = make_uint2(0, 0);
-    if constexpr (VEC) {
-      if (n < N) u = *reinterpret_cast<const uint2*>(q);
-    } else {
-      if (n < N) u.x = q[0];
-      if (n + 1 < N) u.x |= uint32_t(q[1]) << 16;
-      if (n + 2 < N) u.y = q[2];
-      if (n + 3 < N) u.y |= uint32_t(q[3]) << 16;
-    }
-    v[0] = __uint_as_float(u.x << 16);
-    v[1] = __uint_as_float(u.x & 0xffff0000u);
-    v[2] = __uint_as_float(u.y << 16);
-    v[3] = __uint_as_float(u.y & 0xffff0000u);
-  } else {
-    const float* q = static_cast<const float*>(y) + at;
-    v = f32x4{0.f, 0.f, 0.f, 0.f};
-    if constexpr (VEC) {
-      if (n < N) v = *reinterpret_cast<const f32x4*>(q);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < N) v[i] = q[i];
-    }
-  }
-  return v;
+__device__ __forceinline__ f32x4 as_f32(uint2 u) {
+  return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+               __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)};
 }
+__device__ __forceinline__ f32x4 as_f32(f32x4 v) { return v; }
 
 template <bool BF16, bool VEC>
 __device__ __forceinline__ void store_y(void* y, size_t at, int n, int N, f32x4 v) {
@@ -235,7 +222,8 @@ template <int RP>
 struct Parts {
   static constexpr int OCT = RP / 8, NM = (3 * OCT + 3) / 4;
   static constexpr int NB = RP >= 32 ? RP / 32 : NM;     // different operands of B among the NM
-  static constexpr int LD = 32 * NM + 8;                 // bf16 a row in LDS
+  static constexpr int LD = 32 * NM + 8;                 // bf16 a row of t in LDS
+  static constexpr int kB = OCT * 1024;                  // bytes of 64 rows of B in LDS
 };
 
 // Ranks j .. j + 3 of a row of t, in three parts.
@@ -270,72 +258,131 @@ __device__ __forceinline__ void clear_tail(uint16_t* ts, int tid, int threads) {
     for (int i = tid; i < MS * 16 * kTail; i += threads) ts[i / kTail * P::LD + 3 * RP + i % kTail] = 0;
 }
 
+// 64 rows of B (columns of y) go through LDS as x and A do: memory holds them in
+// one piece, and an operand's lane wants an octet of every fourth row.  Octet o
+// of row n lies at 16 (64 o + 16 (n & 3) + (n >> 2 ^ s)), with s made of n & 3 and
+// o so that sixteen neighbours in memory are sixteen different bank groups.
+template <int OCT>
+__device__ __forceinline__ int b_slot(int n, int o) {
+  const int s = (n & 3) << 2 ^ (OCT == 2 ? o << 1 : (o & 3) ^ (o & 4) << 1 ^ (o & 8) >> 1);
+  return 16 * (64 * o + 16 * (n & 3) + ((n >> 2) ^ s));
+}
+
+// In flight: 16-byte units, or (where rows of B are no whole units) elements.
 template <int RP, bool VECB>
-__device__ __forceinline__ void load_bv(const LoraProblem& p, const Tile& t, int n0,
-                                        uint4 (&bv)[Parts<RP>::NB][4]) {
-  using P = Parts<RP>;
-  const int lane = lane_id(), c = lane & 15, g = lane >> 4;
+using RawB = std::conditional_t<VECB, u32x4[RP / 8], u32x4[1]>;
+
+template <int RP, bool VECB>
+__device__ __forceinline__ void load_b(const LoraProblem& p, const Tile& t, int n0,
+                                       RawB<RP, VECB>& v) {
+  if constexpr (VECB) {
+    constexpr int OCT = RP / 8;
+    const int ro = p.r / 8, lane = lane_id();
+    const uint16_t* b = p.b + (size_t(t.e) * p.N + n0) * p.r;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int n = min(n0 + 4 * c + j, p.N - 1);
-    const uint16_t* br = p.b + (size_t(t.e) * p.N + n) * p.r;
-#pragma unroll
-    for (int q = 0; q < P::NB; ++q) {
-      const int oct = 4 * q + g;
-      bv[q][j] = load_b<VECB>(br, oct % P::OCT, p.r);
-      if (oct >= 3 * P::OCT) bv[q][j] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < OCT; ++i) {
+      const int u = 64 * i + lane, n = min(u / OCT, p.N - 1 - n0), o = min(u % OCT, ro - 1);
+      v[i] = *reinterpret_cast<const u32x4*>(b + 8 * (n * ro + o));
     }
   }
 }
 
-// columns n0 .. n0 + 63 of the tile
-template <int RP, int MS, bool BF16, bool VECY>
-__device__ __forceinline__ void expand_cols(const LoraProblem& p, const uint16_t* ts, int n0,
-                                            const int (&row)[MS][4],
-                                            const uint4 (&bv)[Parts<RP>::NB][4]) {
-  using P = Parts<RP>;
-  const int lane = lane_id(), c = lane & 15, g = lane >> 4;
-  const int n = n0 + 4 * c;
-  constexpr int G = MS > 1 && VECY ? 2 : 1;      // row tiles whose y is in flight together
+// past the rank 0
+template <int RP, bool VECB>
+__device__ __forceinline__ void put_b(const LoraProblem& p, const Tile& t, int n0, char* bs,
+                                      const RawB<RP, VECB>& v) {
+  constexpr int OCT = RP / 8;
+  const int lane = lane_id();
+  if constexpr (VECB) {
 #pragma unroll
-  for (int m0 = 0; m0 < MS; m0 += G) {
-    f32x4 yv[G][4];
+    for (int i = 0; i < OCT; ++i) {
+      const int u = 64 * i + lane, o = u % OCT;
+      *reinterpret_cast<u32x4*>(bs + b_slot<OCT>(u / OCT, o)) = 8 * o < p.r ? v[i] : u32x4{0, 0, 0, 0};
+    }
+  } else {
+    const uint16_t* b = p.b + (size_t(t.e) * p.N + n0) * p.r;
+#pragma unroll 1
+    for (int i0 = 0; i0 < RP; i0 += 8) {
+      uint16_t h[8];
 #pragma unroll
-    for (int m = 0; m < G; ++m)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int at = row[m0 + m][q];
-        yv[m][q] = load_y<BF16, VECY>(p.y, size_t(max(at, 0)) * p.N + n, at < 0 ? p.N : n, p.N);
+      for (int i = 0; i < 8; ++i) {
+        const int x = 64 * (i0 + i) + lane;
+        h[i] = b[min(x / RP, p.N - 1 - n0) * p.r + min(x % RP, p.r - 1)];
       }
 #pragma unroll
-    for (int m = 0; m < G; ++m) {
-      f32x4 acc[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int q = 0; q < P::NM; ++q) {
-        const uint4 tv = *reinterpret_cast<const uint4*>(ts + (16 * (m0 + m) + c) * P::LD + 32 * q + 8 * g);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = mfma(tv, bv[q % P::NB][j], acc[j]);
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int at = row[m0 + m][q];
-        const f32x4 d = {acc[0][q], acc[1][q], acc[2][q], acc[3][q]};
-        if (at >= 0) store_y<BF16, VECY>(p.y, size_t(at) * p.N + n, n, p.N, yv[m][q] + d);
+      for (int i = 0; i < 8; ++i) {
+        const int x = 64 * (i0 + i) + lane, j = x % RP;
+        *reinterpret_cast<uint16_t*>(bs + b_slot<OCT>(x / RP, j >> 3) + 2 * (j & 7)) = j < p.r ? h[i] : uint16_t(0);
       }
     }
-    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-template <int MS>
-__device__ __forceinline__ void rows_of(const LoraProblem& p, const Tile& t, int (&row)[MS][4]) {
-  const int g = lane_id() >> 4;
+// The operand of product j: octet oct of K, row 4 c + j.  Octets past the three
+// parts meet zeros of t.
+template <int RP>
+__device__ __forceinline__ uint4 get_b(const char* bs, int oct, int j) {
+  constexpr int OCT = RP / 8;
+  return *reinterpret_cast<const uint4*>(bs + b_slot<OCT>(4 * (lane_id() & 15) + j, oct % OCT));
+}
+
+// y at the columns n0 .. n0 + 63 of the tile
+template <int MS, bool BF16, bool VECY>
+__device__ __forceinline__ void load_cols(const LoraProblem& p, int n0, const i32x4* rows,
+                                          RawY<BF16> (&yv)[MS][4]) {
+  const int lane = lane_id(), n = n0 + 4 * (lane & 15);
 #pragma unroll
   for (int m = 0; m < MS; ++m)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) row[m][q] = row_at(p, t, 16 * m + 4 * g + q);
+    for (int q = 0; q < 4; ++q) {
+      const int at = rows[4 * m + (lane >> 4)][q];
+      yv[m][q] = load_y<BF16, VECY>(p.y, size_t(max(at, 0)) * p.N, n, p.N);
+    }
+}
+
+// and their sums with B_s t
+template <int RP, int MS, bool BF16, bool VECY>
+__device__ __forceinline__ void expand_cols(const LoraProblem& p, const uint16_t* ts, const char* bs,
+                                            int n0, const i32x4* rows,
+                                            const RawY<BF16> (&yv)[MS][4]) {
+  using P = Parts<RP>;
+  const int lane = lane_id(), c = lane & 15, g = lane >> 4;
+  const int n = n0 + 4 * c;
+  f32x4 acc[MS][4];
+#pragma unroll
+  for (int m = 0; m < MS; ++m)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int b = 0; b < P::NB; ++b) {
+    uint4 bv[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bv[j] = get_b<RP>(bs, 4 * b + g, j);
+#pragma unroll
+    for (int q = b; q < P::NM; q += P::NB)       // the parts that meet this piece of B
+#pragma unroll
+      for (int m = 0; m < MS; ++m) {
+        const uint4 tv = *reinterpret_cast<const uint4*>(ts + (16 * m + c) * P::LD + 32 * q + 8 * g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[m][j] = mfma(tv, bv[j], acc[m][j]);
+      }
+    if (MS * RP > 64) __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int m = 0; m < MS; ++m)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int at = rows[4 * m + g][q];
+      const f32x4 d = {acc[m][0][q], acc[m][1][q], acc[m][2][q], acc[m][3][q]};
+      if (at >= 0) store_y<BF16, VECY>(p.y, size_t(at) * p.N + n, n, p.N, as_f32(yv[m][q]) + d);
+    }
+}
+
+// The rows of a tile, in LDS: kept in registers, they and the addresses made of
+// them take the 40 that a workgroup of 16 waves does not have.
+template <int MS>
+__device__ __forceinline__ void put_rows(const LoraProblem& p, const Tile& t, i32x4* rows) {
+  if (threadIdx.x < MS * 16) reinterpret_cast<int*>(rows)[threadIdx.x] = row_at(p, t, threadIdx.x);
 }
 
 template <int RP, int MS, bool BF16, bool VECB, bool VECY>
@@ -345,13 +392,16 @@ __global__ __launch_bounds__(kWaves * kWave) void k_lora_expand(LoraProblem p, i
   constexpr int kItems = MS * 16 * RP / 4;               // four ranks of a row
   constexpr int kEach = (kItems + kThreads - 1) / kThreads;
   __shared__ __attribute__((aligned(16))) uint16_t ts[MS * 16 * P::LD];
+  __shared__ __attribute__((aligned(16))) char bstage[kWaves * P::kB];
+  __shared__ i32x4 rows[MS * 4];
   Tile t;
   if (!find_tile(p.offsets, p.S, 16 * MS, blockIdx.x, t)) return;
   const int wave = threadIdx.x >> 6;
   const int step = gridDim.y * kWaves * kCols;
   int n0 = (blockIdx.y * kWaves + wave) * kCols;
-  uint4 bv[P::NB][4];
-  if (n0 < p.N) load_bv<RP, VECB>(p, t, n0, bv);
+  char* bs = bstage + wave * P::kB;
+  RawB<RP, VECB> bv;
+  if (n0 < p.N) load_b<RP, VECB>(p, t, n0, bv);
   const float scale = p.scale ? p.scale[t.e] : 1.f;
   const float* src[kEach];
   f32x4 sum[kEach];
@@ -379,13 +429,16 @@ __global__ __launch_bounds__(kWaves * kWave) void k_lora_expand(LoraProblem p, i
     if (it < kItems) put_t<RP>(ts + it / (RP / 4) * P::LD, 4 * (it % (RP / 4)), p.r, scale, sum[i]);
   }
   clear_tail<RP, MS>(ts, threadIdx.x, kThreads);
-  int row[MS][4];
-  rows_of(p, t, row);
+  put_rows<MS>(p, t, rows);
   __syncthreads();
   while (n0 < p.N) {
-    expand_cols<RP, MS, BF16, VECY>(p, ts, n0, row, bv);
+    put_b<RP, VECB>(p, t, n0, bs, bv);
+    RawY<BF16> yv[MS][4];
+    load_cols<MS, BF16, VECY>(p, n0, rows, yv);
+    const int n = n0;
     n0 += step;
-    if (n0 < p.N) load_bv<RP, VECB>(p, t, n0, bv);
+    if (n0 < p.N) load_b<RP, VECB>(p, t, n0, bv);
+    expand_cols<RP, MS, BF16, VECY>(p, ts, bs, n, rows, yv);
   }
 }
 
@@ -397,8 +450,11 @@ template <int RP, int MS>
 struct FusedLds {
   static constexpr int NR = (RP + 15) / 16;
   static constexpr int kStage = (MS + NR) * 1024, kRed = MS * NR * 1024;
-  static constexpr int kWork = kFusedWaves * (kStage > kRed ? kStage : kRed);
-  static constexpr int kBytes = kWork + MS * 16 * Parts<RP>::LD * 2;
+  static constexpr int kB = Parts<RP>::kB;
+  static constexpr int kMost = kStage > kRed ? kStage : kRed;
+  static constexpr int kWork = kFusedWaves * (kMost > kB ? kMost : kB);
+  static constexpr int kRows = kWork + MS * 16 * Parts<RP>::LD * 2;
+  static constexpr int kBytes = kRows + MS * 16 * 4;
 };
 
 template <int RP, int MS, bool BF16, bool VECB, bool VECY>
@@ -408,20 +464,22 @@ __global__ __launch_bounds__(kFusedWaves * kWave) void k_lora_fused(LoraProblem 
   constexpr int NR = L::NR;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   uint16_t* ts = reinterpret_cast<uint16_t*>(smem + L::kWork);
+  i32x4* rows = reinterpret_cast<i32x4*>(smem + L::kRows);
   Tile t;
   if (!find_tile(p.offsets, p.S, 16 * MS, blockIdx.x, t)) return;
   const int lane = lane_id(), wave = threadIdx.x >> 6;
   // column pieces blockIdx.y * chunks + wave, + 16, ...
   const int n1 = min(p.N, int(blockIdx.y + 1) * chunks * kCols);
   int n0 = (blockIdx.y * chunks + wave) * kCols;
-  uint4 bv[P::NB][4];
-  constexpr bool kEarly = P::NB * 4 + MS * NR <= 8;      // registers for B throughout
-  if (kEarly && n0 < n1) load_bv<RP, VECB>(p, t, n0, bv);
+  RawB<RP, VECB> bv;
+  constexpr bool kEarly = RP <= 16;              // registers for B throughout
+  if (kEarly && n0 < n1) load_b<RP, VECB>(p, t, n0, bv);
   const float scale = p.scale ? p.scale[t.e] : 1.f;
   f32x4 acc[MS][NR];
   clear(acc);
   shrink_part(p, t, 32 * wave, p.K, 32 * kFusedWaves, smem + wave * L::kStage, acc);
-  if (!kEarly && n0 < n1) load_bv<RP, VECB>(p, t, n0, bv);
+  constexpr bool kAhead = RP * MS < 64;          // registers for the next of B meanwhile
+  if (kAhead && !kEarly && n0 < n1) load_b<RP, VECB>(p, t, n0, bv);
   __syncthreads();                               // `red` lies where the stages were
   f32x4* red = reinterpret_cast<f32x4*>(smem);
 #pragma unroll
@@ -429,8 +487,7 @@ __global__ __launch_bounds__(kFusedWaves * kWave) void k_lora_fused(LoraProblem 
 #pragma unroll
     for (int j = 0; j < NR; ++j) red[(wave * MS * NR + m * NR + j) * kWave + lane] = acc[m][j];
   clear_tail<RP, MS>(ts, threadIdx.x, kFusedWaves * kWave);
-  int row[MS][4];
-  rows_of(p, t, row);
+  put_rows<MS>(p, t, rows);
   __syncthreads();
   // item (m, j, lane) as the waves hold it: ranks 16 j + 4 g .. + 3 of row 16 m + c
   for (int it = threadIdx.x; it < MS * NR * kWave; it += kFusedWaves * kWave) {
@@ -442,10 +499,18 @@ __global__ __launch_bounds__(kFusedWaves * kWave) void k_lora_fused(LoraProblem 
     if (j < RP) put_t<RP>(ts + (16 * (mj / NR) + (l & 15)) * P::LD, j, p.r, scale, v);
   }
   __syncthreads();
+  char* bs = smem + wave * P::kB;                // and B's rows after that
   while (n0 < n1) {
-    expand_cols<RP, MS, BF16, VECY>(p, ts, n0, row, bv);
+    if (!kAhead) load_b<RP, VECB>(p, t, n0, bv);
+    put_b<RP, VECB>(p, t, n0, bs, bv);
+    __builtin_amdgcn_sched_barrier(0);           // the steps as they stand: 128 registers
+    RawY<BF16> yv[MS][4];
+    load_cols<MS, BF16, VECY>(p, n0, rows, yv);
+    __builtin_amdgcn_sched_barrier(0);
+    const int n = n0;
     n0 += kFusedWaves * kCols;
-    if (n0 < n1) load_bv<RP, VECB>(p, t, n0, bv);
+    if (kAhead && n0 < n1) load_b<RP, VECB>(p, t, n0, bv);
+    expand_cols<RP, MS, BF16, VECY>(p, ts, bs, n, rows, yv);
   }
 }
 
@@ -506,19 +571,19 @@ hipError_t launch_fused(const LoraProblem& p, hipStream_t s) {
   return e != hipSuccess ? e : hipGetLastError();
 }
 
-#ifndef LORA_FORCE
-#define LORA_FORCE 0
-#endif
+// One launch wherever it is not much slower: a workgroup reads (ms + nr) 32 K bytes
+// for its t, at 60 to 80 GB/s, and every range of columns reads them again.  With
+// a workgroup for nearly every CU from the row tiles alone there is one range.
 bool fused(const LoraProblem& p) {
-  if (LORA_FORCE == 1) return p.r <= 64 && tile_rows(p) * ((padded(p.r) + 15) / 16) <= 8;
-  if (LORA_FORCE == 2) return false;
   const int ms = tile_rows(p), nr = (padded(p.r) + 15) / 16;
-  return p.r <= 64 && ms * nr <= 8 && int64_t(ms + nr) * 32 * p.K <= 512 * 1024;
+  if (nr > 4) return false;
+  if (LORA_FORCE) return LORA_FORCE == 1;
+  return int64_t(ms + nr) * 32 * p.K <= 512 * 1024 || p.M / (16 * ms) >= 192;
 }
 
 template <int RP, int MS>
 hipError_t launch(const LoraProblem& p, hipStream_t s) {
-  if constexpr (RP <= 64 && MS * ((RP + 15) / 16) <= 8) {
+  if constexpr (RP <= 64) {
     if (fused(p)) return launch_fused<RP, MS>(p, s);
   }
   return launch_two<RP, MS>(p, s);
@@ -526,10 +591,7 @@ hipError_t launch(const LoraProblem& p, hipStream_t s) {
 
 template <int RP>
 hipError_t launch_r(const LoraProblem& p, hipStream_t s) {
-  const int ms = tile_rows(p);
-  if (ms == 1) return launch<RP, 1>(p, s);
-  if (ms == 2) return launch<RP, 2>(p, s);
-  return launch<RP, RP == 128 ? 2 : 4>(p, s);
+  return tile_rows(p) == 1 ? launch<RP, 1>(p, s) : launch<RP, 2>(p, s);
 }
 
 }  // namespace

@@ -649,12 +649,14 @@ def lora_add(x, sorted_rows, offsets, a, b, y, scale=None, workspace=None):
     if scale is not None:
         _want(scale, "scale", torch.float32, (S,), dev)
     if workspace is None:
-        workspace = torch.empty(lora_add_workspace_bytes(M, K, N, S, r), dtype=torch.uint8, device=dev)
+        need = lora_add_workspace_bytes(M, K, N, S, r)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     else:
         _need(workspace, "workspace", torch.uint8, None, dev)
     _enqueue("lora_add", dev, x.data_ptr(), sorted_rows.data_ptr(), offsets.data_ptr(), M, K, N, S, r,
              a.data_ptr(), b.data_ptr(), None if scale is None else scale.data_ptr(), y.data_ptr(),
-             BF16 if dtype == torch.bfloat16 else F32, _ptr(workspace), workspace.numel())
+             BF16 if dtype == torch.bfloat16 else F32, _ptr(workspace),
+             0 if workspace is None else workspace.numel())
     return y
 
 
