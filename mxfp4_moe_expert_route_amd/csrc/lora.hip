@@ -553,8 +553,12 @@ template <int RP, int MS>
 hipError_t launch_fused(const LoraProblem& p, hipStream_t s) {
   const unsigned tiles = unsigned(most_tiles(p, 16 * MS));
   const unsigned cols = unsigned((p.N + kCols - 1) / kCols);
-  unsigned ranges = (255 + tiles) / tiles;
-  ranges = ranges < cols ? ranges : cols;
+  // about one round of workgroups, half a tile an adapter being rounding: 2048 rows
+  // of K = 6144 in one range of columns 21 us, in two 17
+  const int groups = p.M < p.S ? p.M : p.S;
+  const int likely = p.M / (16 * MS) + groups / 2 + 1;
+  unsigned ranges = unsigned((256 + likely / 2) / likely);
+  ranges = ranges < 1 ? 1 : ranges < cols ? ranges : cols;
   const int chunks = int((cols + ranges - 1) / ranges);
   const dim3 grid(tiles, (cols + chunks - 1) / chunks);
   hipError_t e = hipSuccess;

@@ -15,12 +15,12 @@
 //
 // Choices are those of 64 bits: c next to 1 saturates in 32, and a choice that a
 // rounding decides would differ between two ways to compute the same rule.  But
-// 32 bits tell nearly every pair of values apart, so a wave first chooses by
-// fp32 values whose error it knows, and keeps that choice if every two
-// successive values (and the last taken and the first left) are further apart
-// than their errors. Otherwise the order of the nearest candidates is found in fp64, and
-// where that does not settle it the whole choice.  8192 tokens of 384
-// experts in 8 groups: 13 us, 36 in fp64 throughout.
+// 32 bits nearly always settle it.  A wave takes its first k + 2 candidates by
+// fp32 values, orders them by their differences (order_of), which do not lose
+// what the values lose, and keeps the first k if the last of them is further
+// above whatever is no candidate than the values' errors; otherwise it chooses
+// again in fp64.  8192 tokens of 384 experts in 8 groups: 12 us, 36 in fp64
+// throughout; a choice in fp64 at the end of a launch costs it 3.
 #pragma once
 #include "routing.hpp"
 
@@ -113,13 +113,6 @@ struct ScorePlace {
       : lane(lane_id()), lanes(1 << r.lanes_log2), g(lane >> r.lanes_log2), m(lane & (lanes - 1)),
         e0(g * r.size + m) {}
 };
-
-__device__ __forceinline__ double lane_f64(double v, int src) {
-  const uint64_t u = uint64_t(__double_as_longlong(v));
-  const uint32_t lo = __builtin_amdgcn_readlane(int(uint32_t(u)), src);
-  const uint32_t hi = __builtin_amdgcn_readlane(int(uint32_t(u >> 32)), src);
-  return __longlong_as_double((long long)((uint64_t(hi) << 32) | lo));
-}
 
 // exp(l - top), and 1 at the top, be it infinite
 __device__ __forceinline__ double exp_f64(float l, float top) {
@@ -232,6 +225,52 @@ __device__ __forceinline__ void sort_down(uint32_t (&key)[N]) {
         }
 }
 
+// The score of a pick to 2^-21 (softmax: and the error of the sum), and for a
+// sigmoid u = 1 - s as exactly.
+__device__ __forceinline__ float pick_score(float l, float top, float inv, bool sigmoid, float& u) {
+  if (!sigmoid) return exp_down(l == top ? 0.0 : double(l) - double(top)) * inv;
+  const float q = exp_down(-fabs(double(l)));
+  const float a = __builtin_amdgcn_rcpf(1.f + q), b = q * a;
+  u = l < 0.f ? a : b;
+  return l < 0.f ? b : a;
+}
+
+__device__ __forceinline__ float lane_above(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x130, 0xf, 0xf, true));   // wave_shl:1
+}
+
+// Whether this lane's pick comes before the next lane's: 1, -1, or 0 where fp32
+// does not tell.  With h the larger logit of the two and d their distance
+//   sigmoid(h) - sigmoid(h - d) = s(h) u(h - d) (1 - exp(-d)),
+//   softmax the same without u,
+// a product of factors known to 2^-20 (softmax: 2^-17), however close the two
+// scores are.  All lanes call it: a lane reads its neighbour's registers.
+__device__ __forceinline__ int order_of(float l, float b, int id, float s, float u, bool biased,
+                                        bool sigmoid) {
+  const float nl = lane_above(l), nb = lane_above(b), ns = lane_above(s), nu = lane_above(u);
+  const int ni = __float_as_int(lane_above(__int_as_float(id)));
+  const int by_id = id < ni ? 1 : -1;
+  if (!biased) return l > nl ? 1 : l < nl ? -1 : l == nl ? by_id : 0;
+  const bool up = l >= nl;
+  const float d = fabsf(l - nl);
+  float t = 1.f - d * (1.f / 7.f);                // 1 - exp(-d), below 1/2 by its series
+  t = 1.f - d * (1.f / 6.f) * t;
+  t = 1.f - d * (1.f / 5.f) * t;
+  t = 1.f - d * (1.f / 4.f) * t;
+  t = 1.f - d * (1.f / 3.f) * t;
+  t = d * (1.f - d * 0.5f * t);
+  if (!(d < 0.5f)) t = 1.f - __builtin_amdgcn_exp2f(d * -1.4426950408889634f);
+  float ds = (up ? s : ns) * t;
+  if (sigmoid) ds *= up ? nu : u;
+  const float db = b - nb;
+  // values that fp64 does not tell apart are equal: left to it
+  const float err = (sigmoid ? 0x1p-20f : 0x1p-17f) * ds + 0x1p-22f * fabsf(db) +
+                    0x1p-51f * (fabsf(s) + fabsf(b));
+  const float x = (up ? ds : -ds) + db;
+  if (l == nl && b == nb) return by_id;
+  return x > err ? 1 : x < -err ? -1 : 0;
+}
+
 // One token by one whole wave; lanes 0..k-1 end with the j-th choice and its
 // weight.
 template <int NPER>
@@ -258,7 +297,7 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
 #pragma unroll
   for (int i = 0; i < NPER; ++i) v[i] = i < held ? v[i] : __builtin_nanf("");
   // fp32 values and a bound on the scores' error
-  float top = none, total = 1.f;
+  float top = none, total = 1.f, inv = 1.f;
   if (!r.sigmoid) {
     uint32_t t = 0;
 #pragma unroll
@@ -290,7 +329,7 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
       c[i] = v[i] > none ? e : 0.f;
       sum += c[i];
     }
-    const float inv = __builtin_amdgcn_rcpf(wave_sum_f32(sum));
+    inv = __builtin_amdgcn_rcpf(wave_sum_f32(sum));
     ds = 0x1p-18f * inv;
 #pragma unroll
     for (int i = 0; i < NPER; ++i) c[i] *= inv;
@@ -303,7 +342,7 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
       sum += double(c[i]);
     }
     total = float(wave_sum_f64(sum));
-    const float inv = __builtin_amdgcn_rcpf(total);
+    inv = __builtin_amdgcn_rcpf(total);
     ds = 0x1p-20f * inv;
 #pragma unroll
     for (int i = 0; i < NPER; ++i) c[i] *= inv;
@@ -379,56 +418,48 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
                    : (my_src >> r.lanes_log2) * r.size + (my_src & (at.lanes - 1)) +
                          (int(kSlots - (uint32_t(my_key) & kSlots)) << r.lanes_log2);
   };
-  take(r.k + 1);                                  // and the first that is left
+  take(r.k + 2);                                  // and the two that are left first
   my_id = id_of();
-  bool close = false;
-  const uint32_t next = __shfl_down(my_key, 1);
-  if (at.lane < r.k && next) {
-    const uint32_t hi = uint32_t(my_key) & ~kSlots, lo = next & ~kSlots;
-    if (bias) {
-      // 2^SB steps of the image and a rounding of the sum
-      const float x = key_value(hi), y = key_value(lo);
-      const float err = 2.f * ds + float(1u << SB) * 0x1p-22f * (fabsf(x) + fabsf(y));
-      close = !(x - y > err);
-    } else {
-      close = hi == lo;
-    }
-  }
+  float l = row[max(my_id, 0)];
+  float mb = bias ? bias[max(my_id, 0)] : 0.f;
   doubt = __any(doubt);
-  if (!doubt && __any(close)) {
-    // the same groups, but values too close: eight more candidates, and the
-    // candidates' order in fp64.  It stands if the k-th is above whatever is
-    // not among them.
-    take(r.k + 9);
-    my_id = id_of();
-    const float l = row[max(my_id, 0)];
-    double x = l;
-    if (bias) {
-      double sum = 1.0;
-      if (!r.sigmoid) sum = total_f64<NPER>(v, top);
-      x = score_f64(l, top, sum, r.sigmoid) + double(bias[max(my_id, 0)]);
-    }
-    int place = at.lane;                          // stays where it is: no candidate
-    if (at.lane < found) {
-      place = 0;
-      for (int j = 0; j < found; ++j) {
-        const double o = lane_f64(x, j);
-        place += o > x || (o == x && __builtin_amdgcn_readlane(my_id, j) < my_id);
+  if (!doubt) {
+    // the candidates' order by their differences, which fp32 has far more
+    // exactly than the values; neighbours that stand the wrong way change places
+    bool settled = false;
+    float s = 0.f;
+    for (int pass = 0; pass < 4 && !settled; ++pass) {
+      float u = 1.f;
+      if (bias) s = pick_score(l, top, inv, r.sigmoid, u);
+      int way = order_of(l, mb, my_id, s, u, bias != nullptr, r.sigmoid);
+      way = at.lane + 1 < found ? way : 1;
+      if (__any(way == 0)) break;
+      const unsigned long long bad = __ballot(way < 0);
+      settled = bad == 0ull;
+      if (!settled) {                             // of a run of wrong pairs the first
+        const unsigned long long first = bad & ~(bad << 1);
+        const int from = at.lane + int(first >> at.lane & 1) - int(first << 1 >> at.lane & 1);
+        l = __shfl(l, from);
+        mb = __shfl(mb, from);
+        my_id = __shfl(my_id, from);
       }
     }
-    if (!all) {
-      const float left = key_value(__builtin_amdgcn_readlane(my_key, found - 1) | kSlots);
-      const double kth = lane_f64(x, __ffsll((long long)__ballot(place == r.k - 1)) - 1);
-      const double err = bias ? double(ds) + double(float(1u << SB) * 0x1p-22f * fabsf(left)) : 0.0;
-      doubt = !(kth > double(left) + err);
+    doubt = !settled;
+    // and whatever is no candidate has at most the last one's key
+    if (settled && !all && found > r.k) {
+      const float left = key_value(uint32_t(__builtin_amdgcn_readlane(my_key, found - 1)) | kSlots);
+      const float x = bias ? lane_f32(s, r.k - 1) + lane_f32(mb, r.k - 1) : lane_f32(l, r.k - 1);
+      const float err = bias ? 2.f * ds + 0x1p-22f * (fabsf(left) + fabsf(x)) : 0.f;
+      doubt = !(x - left > err);
     }
-    my_id = __builtin_amdgcn_ds_permute(place << 2, my_id);
   }
-  if (doubt) my_id = choose_f64<NPER>(v, b, bias != nullptr, top, r, at);
+  if (doubt) {
+    my_id = choose_f64<NPER>(v, b, bias != nullptr, top, r, at);
+    l = row[max(my_id, 0)];
+  }
   // weights: renormalised ones are relative to the largest score, so that they
   // hold where every s underflows
   const bool has = at.lane < r.k && my_id >= 0;
-  const float l = row[has ? my_id : 0];
   float p;
   if (r.sigmoid) {
     const float q = exp_down(-fabs(double(l)));

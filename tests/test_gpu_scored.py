@@ -145,6 +145,65 @@ def test_unavailable_and_extreme(mm, sigmoid, norm):
             check(mm, logits, k, bias, **rule)
 
 
+# E, k, groups, keep, best: 8, 16, 24 and 32 experts a lane of the kernel for many tokens, and its limits
+LARGE = [(384, 8, 1, 1, 1), (384, 8, 8, 4, 2), (384, 6, 4, 2, 1), (256, 8, 8, 4, 2), (64, 8, 16, 5, 2), (512, 8, 1, 1, 2),
+         (120, 1, 2, 1, 1), (20, 5, 5, 3, 2), (508, 7, 1, 1, 1), (8, 8, 1, 1, 1), (260, 3, 13, 4, 2), (390, 8, 1, 1, 1),
+         (384, 9, 1, 1, 1), (516, 8, 1, 1, 1)]
+
+
+@pytest.mark.parametrize("sigmoid", [True, False], ids=["sigmoid", "softmax"])
+@pytest.mark.parametrize("shape", LARGE, ids=lambda s: "x".join(map(str, s)))
+def test_many_tokens_as_few(mm, shape, sigmoid):
+    """Thousands of tokens take the experts that calls of a few take, which the
+    oracle holds; rows of every awkward kind stand among ordinary ones.  Each
+    side's weights are within 2^-20 of the rule's, and of each other's 2^-19."""
+    E, k, groups, keep, best = shape
+    say("route_scored many as few", shape, sigmoid)
+    rng = np.random.default_rng(list(shape) + [sigmoid, 7])
+    T = 5003
+    logits = rng.normal(0, 1.5, (T, E)).astype(np.float32)
+    odd = rng.permutation(T)[:T // 5]
+    logits[odd] = rng.integers(-2, 3, (len(odd), E))                       # ties
+    i, n = np.inf, np.nan
+    for j, at in enumerate(rng.permutation(T)[:200]):
+        kind = j % 8
+        if kind == 0:
+            logits[at] = -i
+        elif kind == 1:
+            logits[at, rng.random(E) < 0.9] = n
+        elif kind == 2:
+            logits[at, rng.integers(0, E)] = i
+        elif kind == 3:
+            logits[at] -= 1000.0
+        elif kind == 4:
+            logits[at] = np.finfo(np.float32).min
+        elif kind == 5:
+            logits[at, :E // 2] = -i
+        elif kind == 6:
+            logits[at] = 0.5 + rng.permutation(E) * 2.0 ** -24             # one step apart
+        else:
+            logits[at] += 18.0                                              # sigmoids next to 1
+    bias = (rng.integers(-60, 61, E) / (1024 if sigmoid else 1024 * E / 8)).astype(np.float32)
+    big = up(logits)
+    for b, norm in ((bias, True), (None, True), (bias, False), (None, False)):
+        call = dict(bias=up(b), score="sigmoid" if sigmoid else "softmax", groups=groups, topk_groups=keep,
+                    group_best=best, renormalise=norm, scale=2.5)
+        ids, w = (v.cpu().numpy() for v in mm.moe_route_scored(big, k, **call))
+        few = [mm.moe_route_scored(big[s:s + 500].contiguous(), k, **call) for s in range(0, T, 500)]
+        assert np.array_equal(ids, np.concatenate([v[0].cpu().numpy() for v in few]))
+        other = np.concatenate([v[1].cpu().numpy() for v in few]).astype(np.float64)
+        assert np.all(np.abs(w - other) <= 2.0 ** -19 * np.abs(other) + 2.0 ** -148)
+    some = rng.permutation(T)[:60]
+    want, ww = scored.route(logits[some], k, None, sigmoid, groups, keep, best, False, 2.5)
+    assert np.array_equal(ids[some], want)
+    weights_match(w[some], ww)
+    # logits of no vector's alignment
+    flat = torch.empty(T * E + 1, device=DEV)
+    flat[1:] = big.view(-1)
+    got = mm.moe_route_scored(flat[1:].view(T, E), k, **call)
+    assert np.array_equal(got[0].cpu().numpy(), ids)
+
+
 def test_many_tokens(mm):
     """More tokens than a launch has waves, and both sides of every rule on sizes."""
     say("route_scored many tokens")
