@@ -1,7 +1,7 @@
 // Token-to-expert permutation: counts, offsets, sorted pair lists.  The
 // algorithm is permute_block in routing.hpp; this file launches it as one
 // workgroup of 4 waves (up to 1024 pairs) or 16 (up to 8192), and above that
-// as one workgroup per range of pairs (three kernels, below).
+// as one workgroup per range of pairs (one kernel or three, below).
 #include "routing.hpp"
 
 namespace mxm {
@@ -109,6 +109,72 @@ __global__ __launch_bounds__(4 * kWave) void k_perm_scatter(const int32_t* __res
                    pair_to_row, smem, wave_sum);
 }
 
+// Up to kOneMaxPairs pairs of calls with k >= 4: every workgroup counts all pairs
+// for itself, those before its range apart, which gives it the offsets and its
+// bases without another launch (65536 pairs of 384 experts: 9 us, 17 in three
+// launches).  A token's pairs are of different experts, so with k >= 4 at most 16
+// of the 64 that a wave counts at a time meet on one counter.
+constexpr int kOneMaxPairs = 1 << 17;
+constexpr int kOneWaves = 16;
+constexpr int kOneRange = 256;
+constexpr int kOneBatch = 16;                    // ids a thread loads together
+
+// expert counters and bases, then permute_block's tables
+size_t one_lds(int E) { return size_t(2 + kOneWaves + 1) * E * sizeof(int32_t); }
+
+__global__ __launch_bounds__(kOneWaves * kWave) void k_perm_one(const int32_t* __restrict__ ids,
+                                                                int R, int E, int nr,
+                                                                int32_t* __restrict__ counts,
+                                                                int32_t* __restrict__ offsets,
+                                                                int32_t* __restrict__ sorted_pairs,
+                                                                int32_t* __restrict__ pair_to_row) {
+  constexpr int NT = kOneWaves * kWave;
+  extern __shared__ int32_t smem[];
+  __shared__ int32_t wave_sum[kOneWaves];
+  int32_t* count = smem;                         // [0, E): before the range, [E, 2 E): from it on
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
+  int r0, r1;
+  range_of(R, nr, blockIdx.x, r0, r1);
+  for (int e = tid; e < 2 * E; e += NT) count[e] = 0;
+  __syncthreads();
+  for (int p0 = tid; p0 < R; p0 += NT * kOneBatch) {
+    int id[kOneBatch];
+#pragma unroll
+    for (int i = 0; i < kOneBatch; ++i) {
+      const int p = p0 + NT * i;
+      id[i] = ids[min(p, R - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < kOneBatch; ++i) {
+      const int p = p0 + NT * i;
+      if (p < R && unsigned(id[i]) < unsigned(E)) atomicAdd(&count[id[i] + (p < r0 ? 0 : E)], 1);
+    }
+  }
+  __syncthreads();
+  // E <= 1024: one expert a thread
+  const int before = tid < E ? count[tid] : 0;
+  const int total = before + (tid < E ? count[E + tid] : 0);
+  const int incl = wave_incl_scan(total);
+  if (lane == kWave - 1) wave_sum[wave] = incl;
+  __syncthreads();
+  int run = incl - total, all = 0;
+  for (int w = 0; w < kOneWaves; ++w) {
+    run += w < wave ? wave_sum[w] : 0;
+    all += wave_sum[w];
+  }
+  if (tid < E) {
+    count[tid] = run + before;                   // the range's first row of the expert
+    if (blockIdx.x == 0) {
+      counts[tid] = total;
+      offsets[tid] = run;
+    }
+  }
+  if (tid == 0 && blockIdx.x == 0) offsets[E] = all;
+  __syncthreads();
+  permute_block<kOneWaves>(ids, r0, r1, E, count, nullptr, nullptr, sorted_pairs, pair_to_row,
+                           smem + 2 * E, wave_sum);
+}
+
 int ranges_for(int64_t R) {
   if (R <= kSingleMaxPairs) return 0;
   const int64_t n = (R + kRangePairs - 1) / kRangePairs;
@@ -126,6 +192,14 @@ hipError_t launch_permute(const int32_t* ids, int T, int E, int k, int32_t* coun
                           void* workspace, hipStream_t s) {
   const int R = T * k;
   const int nr = ranges_for(R);
+  if (nr > 0 && k >= 4 && R <= kOneMaxPairs) {
+    static std::atomic<bool> set[kMaxDevices];   // 19 E ints, E up to 1024: above 64 KB
+    const hipError_t e = lds_limit_once(reinterpret_cast<const void*>(&k_perm_one), int(one_lds(1024)), set);
+    if (e != hipSuccess) return e;
+    const int n = (R + kOneRange - 1) / kOneRange < 256 ? (R + kOneRange - 1) / kOneRange : 256;
+    k_perm_one<<<n, kOneWaves * kWave, one_lds(E), s>>>(ids, R, E, n, counts, offsets, sorted_pairs, pair_to_row);
+    return hipGetLastError();
+  }
   if (nr > 0) {
     int32_t* ws = static_cast<int32_t*>(workspace);
     k_perm_hist<<<nr, 256, size_t(E) * sizeof(int32_t), s>>>(ids, R, E, nr, ws);

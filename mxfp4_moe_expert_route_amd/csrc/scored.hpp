@@ -114,6 +114,13 @@ struct ScorePlace {
         e0(g * r.size + m) {}
 };
 
+__device__ __forceinline__ double lane_f64(double v, int src) {
+  const uint64_t u = uint64_t(__double_as_longlong(v));
+  const uint32_t lo = __builtin_amdgcn_readlane(int(uint32_t(u)), src);
+  const uint32_t hi = __builtin_amdgcn_readlane(int(uint32_t(u >> 32)), src);
+  return __longlong_as_double((long long)((uint64_t(hi) << 32) | lo));
+}
+
 // exp(l - top), and 1 at the top, be it infinite
 __device__ __forceinline__ double exp_f64(float l, float top) {
   return exp(l == top ? 0.0 : double(l) - double(top));
@@ -136,43 +143,56 @@ __device__ __forceinline__ double total_f64(const float (&v)[NPER], float top) {
   return wave_sum_f64(total);
 }
 
-// The choice in fp64; lanes 0..k-1 end with the j-th id, or -1.  v is NaN in
+// The values c in fp64, -inf where an expert is not available.  v is NaN in
 // slots without an expert, top the row's largest logit.
+template <int NPER>
+__device__ __forceinline__ void values_f64(const float (&v)[NPER], const float (&b)[NPER],
+                                           float top, bool sigmoid, double (&c)[NPER]) {
+  const double none = -__builtin_inf();
+  double total = 1.0;
+  if (!sigmoid) total = total_f64<NPER>(v, top);
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) {
+    const double x = score_f64(v[i], top, total, sigmoid) + double(b[i]);
+    c[i] = double(v[i]) > none && x > none ? x : none;
+    if (i % 2) __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// Whether the lane's group stays, by values in fp64.
+template <int NPER>
+__device__ __forceinline__ bool keep_f64(const double (&c)[NPER], const ScoreRule& r,
+                                         const ScorePlace& at) {
+  const double none = -__builtin_inf();
+  double a1 = none, a2 = none;                    // the two largest of the group
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) {
+    a2 = c[i] > a1 ? a1 : max_f64(a2, c[i]);
+    a1 = max_f64(a1, c[i]);
+  }
+  for (int d = 1; d < at.lanes; d <<= 1) {
+    const double o1 = __shfl_xor(a1, d), o2 = __shfl_xor(a2, d);
+    a2 = o1 > a1 ? max_f64(a1, o2) : max_f64(a2, o1);
+    a1 = max_f64(a1, o1);
+  }
+  const double value = r.best == 2 && a2 > none ? a1 + a2 : a1;
+  int before = 0;
+  for (int j = 0; j < r.groups; ++j) {
+    const double o = lane_f64(value, j << r.lanes_log2);
+    before += o > value || (o == value && j < at.g);
+  }
+  return before < r.keep;
+}
+
+// The choice in fp64; lanes 0..k-1 end with the j-th id, or -1.
 template <int NPER>
 __device__ __forceinline__ int choose_f64(const float (&v)[NPER], const float (&b)[NPER],
                                           bool biased, float top, const ScoreRule& r,
                                           const ScorePlace& at) {
   const double none = -__builtin_inf();
-  double c[NPER];                                 // -inf: not available
-  double total = 1.0;
-  if (!r.sigmoid) total = total_f64<NPER>(v, top);
-#pragma unroll
-  for (int i = 0; i < NPER; ++i) {
-    const double x = score_f64(v[i], top, total, r.sigmoid) + double(b[i]);
-    c[i] = double(v[i]) > none && x > none ? x : none;
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  bool kept = at.g < r.groups;
-  if (r.groups > 1) {
-    double a1 = none, a2 = none;                  // the two largest of the group
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) {
-      a2 = c[i] > a1 ? a1 : max_f64(a2, c[i]);
-      a1 = max_f64(a1, c[i]);
-    }
-    for (int d = 1; d < at.lanes; d <<= 1) {
-      const double o1 = __shfl_xor(a1, d), o2 = __shfl_xor(a2, d);
-      a2 = o1 > a1 ? max_f64(a1, o2) : max_f64(a2, o1);
-      a1 = max_f64(a1, o1);
-    }
-    const double value = r.best == 2 && a2 > none ? a1 + a2 : a1;
-    int before = 0;
-    for (int j = 0; j < r.groups; ++j) {
-      const double o = __shfl(value, j << r.lanes_log2);
-      before += o > value || (o == value && j < at.g);
-    }
-    kept = kept && before < r.keep;
-  }
+  double c[NPER];
+  values_f64(v, b, top, r.sigmoid, c);
+  const bool kept = r.groups == 1 || keep_f64(c, r, at);
   uint64_t key[NPER];
 #pragma unroll
   for (int i = 0; i < NPER; ++i)
@@ -311,9 +331,10 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
   const bool scored = bias || r.groups > 1;       // else logits decide
   float c[NPER], ds = 0.f;
   if (r.sigmoid) {
-    // |error| of s: s (1 - s) (1.5 2^-24 |l| + 2^-23) of the exponential and 1.5
-    // 2^-23 s of the sum and the reciprocal, below 2^-22
-    ds = 0x1p-21f;
+    // |error| of s: s (1 - s) (1.25 2^-24 |l| + 2^-23) of the exponential, whose
+    // instruction is off by a unit in the last place, and 1.5 2^-23 s of the sum
+    // and the reciprocal, a unit too: below 1.9 2^-23 in all
+    ds = 0x1p-22f;
 #pragma unroll
     for (int i = 0; i < NPER; ++i)
       c[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v[i] * -1.4426950408889634f));
@@ -355,7 +376,7 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
     const float x = fmaxf(c[i] + b[i], none);     // NaN: none
     c[i] = v[i] > none ? x : none;
   }
-  bool kept = true, doubt = false;
+  bool kept = true;
   if (r.groups > 1) {
     float a1 = none, a2 = none;                   // the two largest of the group
 #pragma unroll
@@ -374,7 +395,8 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
     if (r.lanes_log2 > 4) meet(across<16>(a1), across<16>(a2));
     const bool two = r.best == 2 && a2 > none;
     const float value = two ? a1 + a2 : a1;
-    const float err = 2.f * ds + 0x1p-22f * (fabsf(a1) + (two ? fabsf(a2) : 0.f));
+    // three roundings of 2^-24: the sums with the bias, the value, and lo and hi
+    const float err = 2.f * ds + 0x1.8p-23f * (fabsf(a1) + (two ? fabsf(a2) : 0.f));
     const float lo = a1 > none ? value - err : none, hi = a1 > none ? value + err : none;
     int surely = 0, maybe = 0;                    // groups before this one
     for (int j = 0; j < r.groups; ++j) {
@@ -382,7 +404,11 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
       maybe += !(lane_f32(hi, j << r.lanes_log2) < lo);          // itself among them
     }
     kept = surely < r.keep;
-    doubt = kept && maybe - 1 >= r.keep && a1 > none;
+    if (__any(kept && maybe - 1 >= r.keep && a1 > none)) {
+      double x[NPER];
+      values_f64(v, b, top, r.sigmoid, x);
+      kept = keep_f64(x, r, at);
+    }
   }
   // keys: the value's order image, its lowest bits the slot
   uint32_t key[NPER];
@@ -422,36 +448,34 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
   my_id = id_of();
   float l = row[max(my_id, 0)];
   float mb = bias ? bias[max(my_id, 0)] : 0.f;
-  doubt = __any(doubt);
-  if (!doubt) {
-    // the candidates' order by their differences, which fp32 has far more
-    // exactly than the values; neighbours that stand the wrong way change places
-    bool settled = false;
-    float s = 0.f;
-    for (int pass = 0; pass < 4 && !settled; ++pass) {
-      float u = 1.f;
-      if (bias) s = pick_score(l, top, inv, r.sigmoid, u);
-      int way = order_of(l, mb, my_id, s, u, bias != nullptr, r.sigmoid);
-      way = at.lane + 1 < found ? way : 1;
-      if (__any(way == 0)) break;
-      const unsigned long long bad = __ballot(way < 0);
-      settled = bad == 0ull;
-      if (!settled) {                             // of a run of wrong pairs the first
-        const unsigned long long first = bad & ~(bad << 1);
-        const int from = at.lane + int(first >> at.lane & 1) - int(first << 1 >> at.lane & 1);
-        l = __shfl(l, from);
-        mb = __shfl(mb, from);
-        my_id = __shfl(my_id, from);
-      }
+  bool doubt = false;
+  // the candidates' order by their differences, which fp32 has far more
+  // exactly than the values; neighbours that stand the wrong way change places
+  bool settled = false;
+  float s = 0.f;
+  for (int pass = 0; pass < 4 && !settled; ++pass) {
+    float u = 1.f;
+    if (bias) s = pick_score(l, top, inv, r.sigmoid, u);
+    int way = order_of(l, mb, my_id, s, u, bias != nullptr, r.sigmoid);
+    way = at.lane + 1 < found ? way : 1;
+    if (__any(way == 0)) break;
+    const unsigned long long bad = __ballot(way < 0);
+    settled = bad == 0ull;
+    if (!settled) {                             // of a run of wrong pairs the first
+      const unsigned long long first = bad & ~(bad << 1);
+      const int from = at.lane + int(first >> at.lane & 1) - int(first << 1 >> at.lane & 1);
+      l = __shfl(l, from);
+      mb = __shfl(mb, from);
+      my_id = __shfl(my_id, from);
     }
-    doubt = !settled;
-    // and whatever is no candidate has at most the last one's key
-    if (settled && !all && found > r.k) {
-      const float left = key_value(uint32_t(__builtin_amdgcn_readlane(my_key, found - 1)) | kSlots);
-      const float x = bias ? lane_f32(s, r.k - 1) + lane_f32(mb, r.k - 1) : lane_f32(l, r.k - 1);
-      const float err = bias ? 2.f * ds + 0x1p-22f * (fabsf(left) + fabsf(x)) : 0.f;
-      doubt = !(x - left > err);
-    }
+  }
+  doubt = !settled;
+  // and whatever is no candidate has at most the last one's key
+  if (settled && !all && found > r.k) {
+    const float left = key_value(uint32_t(__builtin_amdgcn_readlane(my_key, found - 1)) | kSlots);
+    const float x = bias ? lane_f32(s, r.k - 1) + lane_f32(mb, r.k - 1) : lane_f32(l, r.k - 1);
+    const float err = bias ? 2.f * ds + 0x1p-22f * (fabsf(left) + fabsf(x)) : 0.f;
+    doubt = !(x - left > err);
   }
   if (doubt) {
     my_id = choose_f64<NPER>(v, b, bias != nullptr, top, r, at);

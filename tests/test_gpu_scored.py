@@ -305,3 +305,27 @@ def test_layer(mm, small_layer, T):
     tol_check(b.out.cpu().numpy(), want, "scored layer out")
     if T > 1:
         assert not b.out[T - 1].any()
+
+
+# both sides of every limit between the grouping's kernels: 8192 and 131072 pairs, 4 experts a token
+@pytest.mark.parametrize("T,E,k", [(1024, 384, 8), (1025, 384, 8), (2050, 7, 4), (4097, 1024, 4), (5000, 33, 3), (8192, 384, 8),
+                                   (4096, 64, 32), (16384, 384, 8), (16385, 384, 8), (2731, 5, 5), (9001, 1, 1), (2049, 4, 4)])
+def test_grouping_of_many_pairs(mm, T, E, k):
+    say("permute", T, E, k)
+    rng = np.random.default_rng([T, E, k])
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    for kind in range(3):
+        if kind == 1:                                     # some dropped
+            ids = np.where(rng.random((T, k)) < 0.3, rng.choice([-1, E, 2 ** 31 - 1, -2 ** 31], (T, k)), ids).astype(np.int32)
+        elif kind == 2:                                   # all of one expert
+            ids[:] = E - 1
+        got = [v.cpu().numpy() for v in mm.moe_permute(torch.from_numpy(ids).to(DEV), E)]
+        flat = ids.ravel()
+        ok = (flat >= 0) & (flat < E)
+        pairs = np.flatnonzero(ok)
+        pairs = pairs[np.argsort(flat[pairs], kind="stable")]
+        counts = np.bincount(flat[ok], minlength=E)
+        row = np.full(T * k, -1)
+        row[pairs] = np.arange(len(pairs))
+        assert np.array_equal(got[0], counts) and np.array_equal(got[1], np.concatenate([[0], np.cumsum(counts)]))
+        assert np.array_equal(got[2][:len(pairs)], pairs) and np.array_equal(got[3], row)
