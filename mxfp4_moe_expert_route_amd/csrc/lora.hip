@@ -17,9 +17,6 @@ constexpr int kCols = 64;            // columns of y a wave holds at a time
 // rank padded to a size that the kernels are made for
 int padded(int r) { return r <= 8 ? 8 : r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 
-#ifndef LORA_FORCE
-#define LORA_FORCE 0
-#endif
 // row tiles of 16 a workgroup takes: two where that leaves a workgroup for every CU
 int tile_rows(const LoraProblem& p) {
   const int mean = p.M / (p.M < p.S ? p.M : p.S);
@@ -553,12 +550,12 @@ template <int RP, int MS>
 hipError_t launch_fused(const LoraProblem& p, hipStream_t s) {
   const unsigned tiles = unsigned(most_tiles(p, 16 * MS));
   const unsigned cols = unsigned((p.N + kCols - 1) / kCols);
-  // about one round of workgroups, half a tile an adapter being rounding: 2048 rows
-  // of K = 6144 in one range of columns 21 us, in two 17
-  const int groups = p.M < p.S ? p.M : p.S;
-  const int likely = p.M / (16 * MS) + groups / 2 + 1;
-  unsigned ranges = unsigned((256 + likely / 2) / likely);
-  ranges = ranges < 1 ? 1 : ranges < cols ? ranges : cols;
+  // One round of workgroups, those without rows too, which take a CU until they
+  // know it: 2048 rows of K = 6144 in one range of columns 20.7 us, in two (272
+  // workgroups) 17.1; 512 rows of 32 adapters in four ranges (256) 10.3, in five 15.6.
+  unsigned ranges = (255 + tiles) / tiles;
+  if (ranges > 1 && tiles * ranges > 288) --ranges;
+  ranges = ranges < cols ? ranges : cols;
   const int chunks = int((cols + ranges - 1) / ranges);
   const dim3 grid(tiles, (cols + chunks - 1) / chunks);
   hipError_t e = hipSuccess;
@@ -581,7 +578,6 @@ hipError_t launch_fused(const LoraProblem& p, hipStream_t s) {
 bool fused(const LoraProblem& p) {
   const int ms = tile_rows(p), nr = (padded(p.r) + 15) / 16;
   if (nr > 4) return false;
-  if (LORA_FORCE) return LORA_FORCE == 1;
   return int64_t(ms + nr) * 32 * p.K <= 512 * 1024 || p.M / (16 * ms) >= 192;
 }
 

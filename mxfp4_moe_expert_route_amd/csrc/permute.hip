@@ -2,7 +2,7 @@
 // algorithm is permute_block in routing.hpp; this file launches it as one
 // workgroup of 4 waves (up to 1024 pairs) or 16 (up to 8192), and above that
 // as one workgroup per range of pairs (one kernel or three, below).
-#include "routing.hpp"
+#include "scored.hpp"
 
 namespace mxm {
 namespace {
@@ -122,35 +122,12 @@ constexpr int kOneBatch = 16;                    // ids a thread loads together
 // expert counters and bases, then permute_block's tables
 size_t one_lds(int E) { return size_t(2 + kOneWaves + 1) * E * sizeof(int32_t); }
 
-__global__ __launch_bounds__(kOneWaves * kWave) void k_perm_one(const int32_t* __restrict__ ids,
-                                                                int R, int E, int nr,
-                                                                int32_t* __restrict__ counts,
-                                                                int32_t* __restrict__ offsets,
-                                                                int32_t* __restrict__ sorted_pairs,
-                                                                int32_t* __restrict__ pair_to_row) {
-  constexpr int NT = kOneWaves * kWave;
-  extern __shared__ int32_t smem[];
-  __shared__ int32_t wave_sum[kOneWaves];
-  int32_t* count = smem;                         // [0, E): before the range, [E, 2 E): from it on
+// From how many pairs of each expert lie before the range (count[0, E)) and in it
+// or past it (count[E, 2 E)): counts, offsets, and in count[0, E) the range's
+// first row of each expert.  By the whole workgroup.
+__device__ __forceinline__ void bases_from_counts(int32_t* count, int E, int32_t* counts,
+                                                  int32_t* offsets, int32_t* wave_sum) {
   const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
-  int r0, r1;
-  range_of(R, nr, blockIdx.x, r0, r1);
-  for (int e = tid; e < 2 * E; e += NT) count[e] = 0;
-  __syncthreads();
-  for (int p0 = tid; p0 < R; p0 += NT * kOneBatch) {
-    int id[kOneBatch];
-#pragma unroll
-    for (int i = 0; i < kOneBatch; ++i) {
-      const int p = p0 + NT * i;
-      id[i] = ids[min(p, R - 1)];
-    }
-#pragma unroll
-    for (int i = 0; i < kOneBatch; ++i) {
-      const int p = p0 + NT * i;
-      if (p < R && unsigned(id[i]) < unsigned(E)) atomicAdd(&count[id[i] + (p < r0 ? 0 : E)], 1);
-    }
-  }
-  __syncthreads();
   // E <= 1024: one expert a thread
   const int before = tid < E ? count[tid] : 0;
   const int total = before + (tid < E ? count[E + tid] : 0);
@@ -163,7 +140,7 @@ __global__ __launch_bounds__(kOneWaves * kWave) void k_perm_one(const int32_t* _
     all += wave_sum[w];
   }
   if (tid < E) {
-    count[tid] = run + before;                   // the range's first row of the expert
+    count[tid] = run + before;
     if (blockIdx.x == 0) {
       counts[tid] = total;
       offsets[tid] = run;
@@ -171,8 +148,98 @@ __global__ __launch_bounds__(kOneWaves * kWave) void k_perm_one(const int32_t* _
   }
   if (tid == 0 && blockIdx.x == 0) offsets[E] = all;
   __syncthreads();
-  permute_block<kOneWaves>(ids, r0, r1, E, count, nullptr, nullptr, sorted_pairs, pair_to_row,
+}
+
+__global__ __launch_bounds__(kOneWaves * kWave) void k_perm_one(const int32_t* __restrict__ ids,
+                                                                int R, int E, int nr,
+                                                                int32_t* __restrict__ counts,
+                                                                int32_t* __restrict__ offsets,
+                                                                int32_t* __restrict__ sorted_pairs,
+                                                                int32_t* __restrict__ pair_to_row) {
+  constexpr int NT = kOneWaves * kWave;
+  extern __shared__ int32_t smem[];
+  __shared__ int32_t wave_sum[kOneWaves];
+  const int tid = threadIdx.x;
+  int r0, r1;
+  range_of(R, nr, blockIdx.x, r0, r1);
+  for (int e = tid; e < 2 * E; e += NT) smem[e] = 0;
+  __syncthreads();
+  for (int p0 = tid; p0 < R; p0 += NT * kOneBatch) {
+    int id[kOneBatch];
+#pragma unroll
+    for (int i = 0; i < kOneBatch; ++i) id[i] = ids[min(p0 + NT * i, R - 1)];
+#pragma unroll
+    for (int i = 0; i < kOneBatch; ++i) {
+      const int p = p0 + NT * i;
+      if (p < R && unsigned(id[i]) < unsigned(E)) atomicAdd(&smem[id[i] + (p < r0 ? 0 : E)], 1);
+    }
+  }
+  __syncthreads();
+  bases_from_counts(smem, E, counts, offsets, wave_sum);
+  permute_block<kOneWaves>(ids, r0, r1, E, smem, nullptr, nullptr, sorted_pairs, pair_to_row,
                            smem + 2 * E, wave_sum);
+}
+
+// The same from the counts of every kCountTokens tokens, a byte an expert (E a
+// multiple of 4, up to kCountExperts), that the routing left: four experts a
+// thread, two sums of 16 bits to a register.  A token's experts are all different,
+// so within the range a pair's rank is the number of lower bits in its expert's
+// mask of tokens.
+__global__ __launch_bounds__(kOneWaves * kWave) void k_perm_counted(
+    const int32_t* __restrict__ ids, int R, int E, int k, const uint32_t* __restrict__ bytes, int rows,
+    int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_pairs,
+    int32_t* __restrict__ pair_to_row) {
+  constexpr int NT = kOneWaves * kWave;
+  extern __shared__ int32_t smem[];
+  __shared__ int32_t wave_sum[kOneWaves];
+  __shared__ uint32_t part[4][kCountExperts / 4];        // even and odd experts, before and from here on
+  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + 2 * E);
+  const int tid = threadIdx.x, cols = E / 4, here = blockIdx.x;
+  const int pair = here * kCountTokens * k + tid;          // of the first kCountTokens k threads
+  const bool owns = tid < kCountTokens * k && pair < R;
+  const int id = owns ? ids[pair] : -1;
+  for (int i = tid; i < kCountExperts; i += NT) (&part[0][0])[i] = 0u;
+  for (int i = tid; i < E; i += NT) mask[i] = 0u;
+  __syncthreads();
+  const bool valid = unsigned(id) < unsigned(E);
+  if (valid) atomicOr(&mask[id], 1u << (tid / k));
+  const int col = tid % cols, parts = NT / cols, mine = tid / cols;
+  if (mine < parts) {
+    uint32_t s[4] = {0u, 0u, 0u, 0u};
+    for (int b0 = mine; b0 < rows; b0 += parts * kOneBatch) {
+      uint32_t v[kOneBatch];
+#pragma unroll
+      for (int i = 0; i < kOneBatch; ++i)
+        v[i] = bytes[size_t(min(b0 + parts * i, rows - 1)) * cols + col];
+#pragma unroll
+      for (int i = 0; i < kOneBatch; ++i) {
+        const int b = b0 + parts * i;
+        const uint32_t x = b < rows ? v[i] : 0u;
+        const uint32_t even = x & 0x00ff00ffu, odd = x >> 8 & 0x00ff00ffu;
+        s[0] += b < here ? even : 0u;
+        s[1] += b < here ? odd : 0u;
+        s[2] += b < here ? 0u : even;
+        s[3] += b < here ? 0u : odd;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) atomicAdd(&part[i][col], s[i]);
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += NT) {
+    const int i = e >> 2, shift = (e & 2) * 8;
+    smem[e] = part[e & 1][i] >> shift & 0xffff;
+    smem[E + e] = part[2 + (e & 1)][i] >> shift & 0xffff;
+  }
+  __syncthreads();
+  bases_from_counts(smem, E, counts, offsets, wave_sum);
+  if (valid) {
+    const int row = smem[id] + __popc(mask[id] & ((1u << (tid / k)) - 1u));
+    sorted_pairs[row] = pair;
+    pair_to_row[pair] = row;
+  } else if (owns) {
+    pair_to_row[pair] = -1;
+  }
 }
 
 int ranges_for(int64_t R) {
@@ -182,6 +249,20 @@ int ranges_for(int64_t R) {
 }
 
 }  // namespace
+
+// an expert's count fits 16 bits
+bool permute_counted_fits(int T, int E) {
+  return T <= kOneMaxPairs / 8 && E % 4 == 0 && E <= kCountExperts;
+}
+
+hipError_t launch_permute_counted(const int32_t* ids, int T, int E, int k, const uint32_t* bytes,
+                                  int32_t* counts, int32_t* offsets, int32_t* sorted_pairs,
+                                  int32_t* pair_to_row, hipStream_t s) {
+  const int rows = (T + kCountTokens - 1) / kCountTokens;
+  k_perm_counted<<<rows, kOneWaves * kWave, size_t(3) * E * sizeof(int32_t), s>>>(ids, T * k, E, k, bytes, rows, counts, offsets,
+                                                            sorted_pairs, pair_to_row);
+  return hipGetLastError();
+}
 
 size_t permute_workspace_bytes(int T, int E, int k) {
   return size_t(ranges_for(int64_t(T) * k)) * E * sizeof(int32_t);

@@ -109,16 +109,14 @@ __device__ __forceinline__ void merge_top8(uint32_t (&a)[8], const uint32_t* b) 
 // lane (g << l2) + m of a row of 16 holds the experts 4 (m + (i << l2)) .. + 3 of
 // group g, i = 0 .. NP / 4 - 1
 template <int NP>
-__global__ __launch_bounds__(256) void k_route_scored_rows(const float* __restrict__ logits,
-                                                           const float* __restrict__ bias, int T,
-                                                           ScoreRule r, int32_t* __restrict__ ids,
-                                                           float* __restrict__ w) {
+__device__ __forceinline__ void score_rows(const float* __restrict__ logits,
+                                           const float* __restrict__ bias, int T, int t0,
+                                           const ScoreRule& r, int32_t* __restrict__ ids,
+                                           float* __restrict__ w, int32_t* hist) {
   constexpr int NV = NP / 4;
   constexpr uint32_t kSlots = 31;
   const float none = -__builtin_inff();
   const int lane = lane_id(), q = lane & 15;
-  const int t0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * kRowTokens;
-  if (t0 >= T) return;                           // whole wave leaves together
   const int t = t0 + (lane >> 4);
   const float* row = logits + int64_t(min(t, T - 1)) * r.E;
   const int l2 = r.lanes_log2 - 2;
@@ -283,6 +281,7 @@ __global__ __launch_bounds__(256) void k_route_scored_rows(const float* __restri
   if (has && t < T && !mine) {
     ids[int64_t(t) * r.k + q] = my_id;
     w[int64_t(t) * r.k + q] = p * r.scale;
+    if (hist) atomicAdd(&hist[my_id], 1);
   }
   for (int i = 0; i < kRowTokens; ++i) {
     if (t0 + i >= T || !((left >> (16 * i)) & 0xffffull)) continue;
@@ -292,47 +291,80 @@ __global__ __launch_bounds__(256) void k_route_scored_rows(const float* __restri
     if (lane < r.k) {
       ids[int64_t(t0 + i) * r.k + lane] = id;
       w[int64_t(t0 + i) * r.k + lane] = f;
+      if (hist && id >= 0) atomicAdd(&hist[id], 1);
     }
   }
 }
 
+template <int NP>
+__global__ __launch_bounds__(256) void k_route_scored_rows(const float* __restrict__ logits,
+                                                           const float* __restrict__ bias, int T,
+                                                           ScoreRule r, int32_t* __restrict__ ids,
+                                                           float* __restrict__ w) {
+  const int t0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * kRowTokens;
+  if (t0 < T) score_rows<NP>(logits, bias, T, t0, r, ids, w, nullptr);
+}
+
+// and how many of the workgroup's 32 tokens took each expert, a byte an expert:
+// the first step of the grouping
+template <int NP>
+__global__ __launch_bounds__(kCountTokens / kRowTokens * kWave) void k_route_scored_count(
+    const float* __restrict__ logits, const float* __restrict__ bias, int T, ScoreRule r,
+    int32_t* __restrict__ ids, float* __restrict__ w, uint32_t* __restrict__ bytes) {
+  constexpr int NT = kCountTokens / kRowTokens * kWave;
+  __shared__ int32_t hist[kCountExperts];
+  for (int e = threadIdx.x; e < r.E; e += NT) hist[e] = 0;
+  __syncthreads();
+  const int t0 = blockIdx.x * kCountTokens + (threadIdx.x >> 6) * kRowTokens;
+  if (t0 < T) score_rows<NP>(logits, bias, T, t0, r, ids, w, hist);
+  __syncthreads();
+  for (int i = threadIdx.x; i < r.E / 4; i += NT)
+    bytes[size_t(blockIdx.x) * (r.E / 4) + i] =
+        hist[4 * i] | hist[4 * i + 1] << 8 | hist[4 * i + 2] << 16 | hist[4 * i + 3] << 24;
+}
+
 // experts that a lane holds
 int per_lane(const ScoreRule& r) { return (r.size + (1 << r.lanes_log2) - 1) >> r.lanes_log2; }
+
+// The kernel of four tokens a wave: whole vectors of logits, four lanes a group at
+// least, of 32 experts at most.  In us, it and a wave a token, 384 experts in 8
+// groups: 2048 tokens 6.5 and 5.6, 4096 6.5 and 7.4, 8192 8.0 and 11.0.
+bool takes_rows(int T, const ScoreRule& r, const float* logits, const float* bias) {
+  return T >= 4096 && r.k <= kRowPicks && r.lanes_log2 >= 2 && per_lane(r) <= 8 && r.size % 4 == 0 &&
+         r.keep * r.size >= r.k + 2 && reinterpret_cast<uintptr_t>(logits) % 16 == 0 &&
+         reinterpret_cast<uintptr_t>(bias) % 16 == 0;
+}
+
+// f(experts that a lane of such a row holds)
+template <class F>
+void by_row_size(const ScoreRule& r, F f) {
+  const int n = per_lane(r);
+  if (n <= 2) f(std::integral_constant<int, 8>());
+  else if (n <= 4) f(std::integral_constant<int, 16>());
+  else if (n <= 6) f(std::integral_constant<int, 24>());
+  else f(std::integral_constant<int, 32>());
+}
 
 }  // namespace
 
 hipError_t launch_route_scored(const float* logits, const float* bias, int T, const ScoreRule& r,
                                int32_t* ids, float* w, hipStream_t s) {
   const int n = per_lane(r);
+  const bool rows = takes_rows(T, r, logits, bias);
   // a launch has fewer than 2^32 threads
   constexpr int kMost = 1 << 25;
-#ifndef ROWS_MIN
-#define ROWS_MIN 4096
-#endif
-  // whole vectors of logits; four lanes a group at least, of 32 experts at most
-  const bool rows = T >= ROWS_MIN && r.k <= kRowPicks && r.lanes_log2 >= 2 && n <= 8 && r.size % 4 == 0 &&
-                    r.keep * r.size >= r.k + 2 && reinterpret_cast<uintptr_t>(logits) % 16 == 0 &&
-                    reinterpret_cast<uintptr_t>(bias) % 16 == 0;
   for (int64_t t0 = 0; t0 < T; t0 += kMost) {
     const int nt = int(T - t0 < kMost ? T - t0 : kMost);
-    if (rows) {
-      auto go = [&](auto per) {
-        k_route_scored_rows<decltype(per)::value><<<(nt + 15) / 16, 256, 0, s>>>(
-            logits + t0 * r.E, bias, nt, r, ids + t0 * r.k, w + t0 * r.k);
-      };
-      if (n <= 2) go(std::integral_constant<int, 8>());
-      else if (n <= 4) go(std::integral_constant<int, 16>());
-      else if (n <= 6) go(std::integral_constant<int, 24>());
-      else go(std::integral_constant<int, 32>());
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-      continue;
-    }
     auto go = [&](auto per) {
       k_route_scored<decltype(per)::value><<<(nt + 3) / 4, 256, 0, s>>>(
           logits + t0 * r.E, bias, nt, r, ids + t0 * r.k, w + t0 * r.k);
     };
-    if (n <= 2) go(std::integral_constant<int, 2>());
+    if (rows)
+      by_row_size(r, [&](auto per) {
+        k_route_scored_rows<decltype(per)::value><<<(nt + 15) / 16, 256, 0, s>>>(
+            logits + t0 * r.E, bias, nt, r, ids + t0 * r.k, w + t0 * r.k);
+      });
+    else if (n <= 2) go(std::integral_constant<int, 2>());
     else if (n <= 4) go(std::integral_constant<int, 4>());
     else if (n <= 6) go(std::integral_constant<int, 6>());
     else if (n <= 8) go(std::integral_constant<int, 8>());
@@ -342,6 +374,21 @@ hipError_t launch_route_scored(const float* logits, const float* bias, int T, co
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+bool route_scored_counts(int T, const ScoreRule& r, const float* logits, const float* bias) {
+  return takes_rows(T, r, logits, bias) && r.k == 8 && permute_counted_fits(T, r.E);
+}
+
+hipError_t launch_route_scored_count(const float* logits, const float* bias, int T,
+                                     const ScoreRule& r, int32_t* ids, float* w, uint32_t* bytes,
+                                     hipStream_t s) {
+  by_row_size(r, [&](auto per) {
+    k_route_scored_count<decltype(per)::value>
+        <<<(T + kCountTokens - 1) / kCountTokens, kCountTokens / kRowTokens * kWave, 0, s>>>(
+            logits, bias, T, r, ids, w, bytes);
+  });
+  return hipGetLastError();
 }
 
 // 16 waves leave a lane 128 registers: enough for eight experts each

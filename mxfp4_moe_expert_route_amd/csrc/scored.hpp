@@ -37,6 +37,19 @@ struct ScoreRule {
 
 hipError_t launch_route_scored(const float* logits, const float* bias, int T, const ScoreRule& r,
                                int32_t* ids, float* w, hipStream_t s);
+// Routing that also counts, for every 32 tokens, how many took each expert (a byte
+// an expert, into the grouping's workspace), and the grouping from those counts:
+// ranges of 256 pairs, so calls of k = 8, whose workspace has the room.
+constexpr int kCountTokens = 32;
+constexpr int kCountExperts = 512;
+bool route_scored_counts(int T, const ScoreRule& r, const float* logits, const float* bias);
+hipError_t launch_route_scored_count(const float* logits, const float* bias, int T,
+                                     const ScoreRule& r, int32_t* ids, float* w, uint32_t* bytes,
+                                     hipStream_t s);
+bool permute_counted_fits(int T, int E);
+hipError_t launch_permute_counted(const int32_t* ids, int T, int E, int k, const uint32_t* bytes,
+                                  int32_t* counts, int32_t* offsets, int32_t* sorted_pairs,
+                                  int32_t* pair_to_row, hipStream_t s);
 // routing and grouping in one workgroup, where it fits
 bool route_scored_fusable(int T, const ScoreRule& r);
 hipError_t launch_route_scored_permute(const float* logits, const float* bias, int T,

@@ -99,6 +99,13 @@ int moe_route_scored_permute(const float* logits, const float* bias, int T, int 
   if (mxm::route_scored_fusable(T, r))
     return launched(mxm::launch_route_scored_permute(logits, bias, T, r, topk_ids, topk_w, counts,
                                                      offsets, sorted_pairs, pair_to_row, s));
+  if (need > 0 && mxm::route_scored_counts(T, r, logits, bias)) {
+    uint32_t* bytes = static_cast<uint32_t*>(workspace);
+    if (mxm::launch_route_scored_count(logits, bias, T, r, topk_ids, topk_w, bytes, s) != hipSuccess)
+      return MXM_ERR_LAUNCH;
+    return launched(mxm::launch_permute_counted(topk_ids, T, E, k, bytes, counts, offsets,
+                                                sorted_pairs, pair_to_row, s));
+  }
   if (mxm::launch_route_scored(logits, bias, T, r, topk_ids, topk_w, s) != hipSuccess)
     return MXM_ERR_LAUNCH;
   return launched(mxm::launch_permute(topk_ids, T, E, k, counts, offsets, sorted_pairs,

@@ -307,6 +307,28 @@ def test_layer(mm, small_layer, T):
         assert not b.out[T - 1].any()
 
 
+@pytest.mark.parametrize("T,E,groups,keep", [(4096, 384, 8, 4), (4127, 384, 1, 1), (8192, 384, 8, 4), (5000, 12, 1, 1),
+                                             (6001, 512, 4, 2), (16384, 64, 1, 1), (16385, 64, 1, 1), (4100, 40, 10, 5)])
+def test_lists_of_many_tokens(mm, T, E, groups, keep):
+    """k = 8: the routing counts for the grouping.  Some tokens have few experts left, or none."""
+    say("route_scored_permute, many tokens", T, E, groups)
+    g = torch.Generator(device=DEV).manual_seed(T + E)
+    logits = torch.randn(T, E, device=DEV, generator=g)
+    logits[::97] = float("-inf")
+    logits[5::89, E // 4:] = float("nan")
+    logits[7::50] = torch.round(logits[7::50])
+    rule = dict(bias=torch.round(torch.randn(E, device=DEV, generator=g) * 30) / 1024, groups=groups, topk_groups=keep)
+    ids, w = mm.moe_route_scored(logits, 8, **rule)
+    assert (ids == -1).any()
+    for ws in (None, torch.full((mm.moe_permute_workspace_bytes(T, E, 8),), 0xff, dtype=torch.uint8, device=DEV)):
+        got = mm.moe_route_scored_permute(logits, 8, **rule, workspace=ws)
+        want = mm.moe_permute(ids, E)
+        n = int(want[1][-1])
+        assert torch.equal(got[0], ids) and torch.equal(got[1], w)
+        assert torch.equal(got[2], want[0]) and torch.equal(got[3], want[1]) and torch.equal(got[5], want[3])
+        assert torch.equal(got[4][:n], want[2][:n])
+
+
 # both sides of every limit between the grouping's kernels: 8192 and 131072 pairs, 4 experts a token
 @pytest.mark.parametrize("T,E,k", [(1024, 384, 8), (1025, 384, 8), (2050, 7, 4), (4097, 1024, 4), (5000, 33, 3), (8192, 384, 8),
                                    (4096, 64, 32), (16384, 384, 8), (16385, 384, 8), (2731, 5, 5), (9001, 1, 1), (2049, 4, 4)])
