@@ -9,7 +9,8 @@ namespace mxm {
 namespace {
 
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
-typedef __attribute__((ext_vector_type(4))) int i32x4;
+typedef __attribute__((ext_vector_type(2))) float f32x2;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2v;
 
 constexpr int kWaves = 4;
 constexpr int kCols = 64;            // columns of y a wave holds at a time
@@ -186,12 +187,13 @@ template <bool BF16, bool VEC>
 __device__ __forceinline__ void store_y(void* y, size_t at, int n, int N, f32x4 v) {
   if constexpr (BF16) {
     uint16_t* q = static_cast<uint16_t*>(y) + at;
-    uint32_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = f32_to_bf16_rne(v[i]);
+    const bf16x2v lo = __builtin_convertvector(f32x2{v[0], v[1]}, bf16x2v);      // to nearest even
+    const bf16x2v hi = __builtin_convertvector(f32x2{v[2], v[3]}, bf16x2v);
+    const uint2 u = make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
     if constexpr (VEC) {
-      if (n < N) *reinterpret_cast<uint2*>(q) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+      if (n < N) *reinterpret_cast<uint2*>(q) = u;
     } else {
+      const uint32_t h[4] = {u.x & 0xffffu, u.x >> 16, u.y & 0xffffu, u.y >> 16};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (n + i < N) q[i] = uint16_t(h[i]);
@@ -219,53 +221,64 @@ template <int RP>
 struct Parts {
   static constexpr int OCT = RP / 8, NM = (3 * OCT + 3) / 4;
   static constexpr int NB = RP >= 32 ? RP / 32 : NM;     // different operands of B among the NM
-  static constexpr int LD = 32 * NM + 8;                 // bf16 a row of t in LDS
+  static constexpr int kT = NM * 1024;                   // bytes of 16 rows of t in LDS
   static constexpr int kB = OCT * 1024;                  // bytes of 64 rows of B in LDS
 };
 
-// Ranks j .. j + 3 of a row of t, in three parts.
+// Where K k .. k + 3 of row i of t lie in LDS: blocks of 1 KB in the order in which
+// an operand's lanes read them (rows one after another read at half that rate).
 template <int RP>
-__device__ __forceinline__ void put_t(uint16_t* row, int j, int r, float scale, f32x4 v) {
+__device__ __forceinline__ int t_slot(int i, int k) {
+  return (i >> 4) * Parts<RP>::kT + 1024 * (k >> 5) + 16 * (16 * (k >> 3 & 3) + (i & 15)) + 2 * (k & 7);
+}
+
+// Ranks j .. j + 3 of row i of t, in three parts.
+template <int RP>
+__device__ __forceinline__ void put_t(char* ts, int i, int j, int r, float scale, f32x4 v) {
   uint32_t part[3][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int e = 0; e < 4; ++e) {
     // past the rank: not t's, and an infinite x times 0 is NaN
-    const float f = j + i < r ? v[i] * scale : 0.f;
+    const float f = j + e < r ? v[e] * scale : 0.f;
     const uint32_t hi = __float_as_uint(f) & 0xffff0000u;
     // an infinite or NaN t has no parts below
     const bool fin = (hi & 0x7f800000u) != 0x7f800000u;
     const float rest = fin ? f - __uint_as_float(hi) : 0.f;
     const uint32_t mid = __float_as_uint(rest) & 0xffff0000u;
-    part[0][i] = hi;
-    part[1][i] = mid;
-    part[2][i] = __float_as_uint(rest - __uint_as_float(mid));
+    part[0][e] = hi;
+    part[1][e] = mid;
+    part[2][e] = __float_as_uint(rest - __uint_as_float(mid));
   }
 #pragma unroll
   for (int s = 0; s < 3; ++s)
-    *reinterpret_cast<uint2*>(row + s * RP + j) =
+    *reinterpret_cast<uint2*>(ts + t_slot<RP>(i, s * RP + j)) =
         make_uint2(part[s][0] >> 16 | (part[s][1] & 0xffff0000u), part[s][2] >> 16 | (part[s][3] & 0xffff0000u));
 }
 
-// the rest of a row of `ts`, up to the instruction's K
+// the rest of a row of t, up to the instruction's K
 template <int RP, int MS>
-__device__ __forceinline__ void clear_tail(uint16_t* ts, int tid, int threads) {
-  using P = Parts<RP>;
-  constexpr int kTail = 32 * P::NM - 3 * RP;
+__device__ __forceinline__ void clear_tail(char* ts, int tid, int threads) {
+  constexpr int kTail = (32 * Parts<RP>::NM - 3 * RP) / 4;
   if constexpr (kTail > 0)
-    for (int i = tid; i < MS * 16 * kTail; i += threads) ts[i / kTail * P::LD + 3 * RP + i % kTail] = 0;
+    for (int i = tid; i < MS * 16 * kTail; i += threads)
+      *reinterpret_cast<uint2*>(ts + t_slot<RP>(i / kTail, 3 * RP + 4 * (i % kTail))) = make_uint2(0, 0);
 }
 
 // 64 rows of B (columns of y) go through LDS as x and A do: memory holds them in
 // one piece, and an operand's lane wants an octet of every fourth row.  Octet o
-// of row n lies at 16 (64 o + 16 (n & 3) + (n >> 2 ^ s)), with s made of n & 3 and
-// o so that sixteen neighbours in memory are sixteen different bank groups.
+// of row n lies at 16 (64 o + 16 (n & 3) + (n >> 2 ^ s)), s = (n & 3) << 2 ^ f(o),
+// so that sixteen neighbours in memory are sixteen different bank groups.  All
+// terms are disjoint bits or combined by ^, so the places of one lane differ by ^
+// of constants.
+__device__ __forceinline__ constexpr int b_swizzle(int oct, int o) {
+  return oct == 2 ? o << 1 : (o & 3) ^ (o & 4) << 1 ^ (o & 8) >> 1;
+}
 template <int OCT>
 __device__ __forceinline__ int b_slot(int n, int o) {
-  const int s = (n & 3) << 2 ^ (OCT == 2 ? o << 1 : (o & 3) ^ (o & 4) << 1 ^ (o & 8) >> 1);
-  return 16 * (64 * o + 16 * (n & 3) + ((n >> 2) ^ s));
+  return 16 * (64 * o + 16 * (n & 3) + ((n >> 2) ^ ((n & 3) << 2) ^ b_swizzle(OCT, o)));
 }
 
-// In flight: 16-byte units, or (where rows of B are no whole units) elements.
+// In flight: 16-byte units, or nothing where rows of B are no whole units.
 template <int RP, bool VECB>
 using RawB = std::conditional_t<VECB, u32x4[RP / 8], u32x4[1]>;
 
@@ -274,12 +287,17 @@ __device__ __forceinline__ void load_b(const LoraProblem& p, const Tile& t, int 
                                        RawB<RP, VECB>& v) {
   if constexpr (VECB) {
     constexpr int OCT = RP / 8;
-    const int ro = p.r / 8, lane = lane_id();
+    const int ro = p.r / 8, lane = lane_id(), n = lane / OCT, o = min(lane % OCT, ro - 1);
     const uint16_t* b = p.b + (size_t(t.e) * p.N + n0) * p.r;
+    if (n0 + 64 <= p.N) {
+      const uint16_t* at = b + 8 * (n * ro + o);
 #pragma unroll
-    for (int i = 0; i < OCT; ++i) {
-      const int u = 64 * i + lane, n = min(u / OCT, p.N - 1 - n0), o = min(u % OCT, ro - 1);
-      v[i] = *reinterpret_cast<const u32x4*>(b + 8 * (n * ro + o));
+      for (int i = 0; i < OCT; ++i)
+        v[i] = *reinterpret_cast<const u32x4*>(at + i * (64 / OCT) * p.r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < OCT; ++i)
+        v[i] = *reinterpret_cast<const u32x4*>(b + 8 * (min(64 / OCT * i + n, p.N - 1 - n0) * ro + o));
     }
   }
 }
@@ -291,11 +309,10 @@ __device__ __forceinline__ void put_b(const LoraProblem& p, const Tile& t, int n
   constexpr int OCT = RP / 8;
   const int lane = lane_id();
   if constexpr (VECB) {
+    const int o = lane % OCT, at = b_slot<OCT>(lane / OCT, o);
 #pragma unroll
-    for (int i = 0; i < OCT; ++i) {
-      const int u = 64 * i + lane, o = u % OCT;
-      *reinterpret_cast<u32x4*>(bs + b_slot<OCT>(u / OCT, o)) = 8 * o < p.r ? v[i] : u32x4{0, 0, 0, 0};
-    }
+    for (int i = 0; i < OCT; ++i)
+      *reinterpret_cast<u32x4*>(bs + (at ^ 256 / OCT * i)) = 8 * o < p.r ? v[i] : u32x4{0, 0, 0, 0};
   } else {
     const uint16_t* b = p.b + (size_t(t.e) * p.N + n0) * p.r;
 #pragma unroll 1
@@ -315,32 +332,35 @@ __device__ __forceinline__ void put_b(const LoraProblem& p, const Tile& t, int n
   }
 }
 
-// The operand of product j: octet oct of K, row 4 c + j.  Octets past the three
-// parts meet zeros of t.
+// The operand of product j: octet 4 q + g (of OCT) of K, row 4 c + j.  Octets past
+// the three parts meet zeros of t.
 template <int RP>
-__device__ __forceinline__ uint4 get_b(const char* bs, int oct, int j) {
+__device__ __forceinline__ uint4 get_b(const char* bs, int q, int j) {
   constexpr int OCT = RP / 8;
-  return *reinterpret_cast<const uint4*>(bs + b_slot<OCT>(4 * (lane_id() & 15) + j, oct % OCT));
+  const int lane = lane_id(), c = lane & 15, g = lane >> 4;
+  const int first = b_slot<OCT>(4 * c, g % OCT);
+  const int step = OCT < 4 ? 0 : 4096 * q ^ 16 * b_swizzle(OCT, 4 * q);
+  return *reinterpret_cast<const uint4*>(bs + (first ^ step ^ 320 * j));
 }
 
 // y at the columns n0 .. n0 + 63 of the tile
 template <int MS, bool BF16, bool VECY>
-__device__ __forceinline__ void load_cols(const LoraProblem& p, int n0, const i32x4* rows,
+__device__ __forceinline__ void load_cols(const LoraProblem& p, int n0, const int64_t* rows,
                                           RawY<BF16> (&yv)[MS][4]) {
   const int lane = lane_id(), n = n0 + 4 * (lane & 15);
 #pragma unroll
   for (int m = 0; m < MS; ++m)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int at = rows[4 * m + (lane >> 4)][q];
-      yv[m][q] = load_y<BF16, VECY>(p.y, size_t(max(at, 0)) * p.N, n, p.N);
+      const int64_t at = rows[16 * m + 4 * (lane >> 4) + q];
+      yv[m][q] = load_y<BF16, VECY>(p.y, size_t(at < 0 ? 0 : at), n, p.N);
     }
 }
 
 // and their sums with B_s t
 template <int RP, int MS, bool BF16, bool VECY>
-__device__ __forceinline__ void expand_cols(const LoraProblem& p, const uint16_t* ts, const char* bs,
-                                            int n0, const i32x4* rows,
+__device__ __forceinline__ void expand_cols(const LoraProblem& p, const char* ts, const char* bs,
+                                            int n0, const int64_t* rows,
                                             const RawY<BF16> (&yv)[MS][4]) {
   using P = Parts<RP>;
   const int lane = lane_id(), c = lane & 15, g = lane >> 4;
@@ -354,12 +374,12 @@ __device__ __forceinline__ void expand_cols(const LoraProblem& p, const uint16_t
   for (int b = 0; b < P::NB; ++b) {
     uint4 bv[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) bv[j] = get_b<RP>(bs, 4 * b + g, j);
+    for (int j = 0; j < 4; ++j) bv[j] = get_b<RP>(bs, b, j);
 #pragma unroll
     for (int q = b; q < P::NM; q += P::NB)       // the parts that meet this piece of B
 #pragma unroll
       for (int m = 0; m < MS; ++m) {
-        const uint4 tv = *reinterpret_cast<const uint4*>(ts + (16 * m + c) * P::LD + 32 * q + 8 * g);
+        const uint4 tv = *reinterpret_cast<const uint4*>(ts + m * P::kT + 1024 * q + 16 * lane);
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[m][j] = mfma(tv, bv[j], acc[m][j]);
       }
@@ -369,17 +389,21 @@ __device__ __forceinline__ void expand_cols(const LoraProblem& p, const uint16_t
   for (int m = 0; m < MS; ++m)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int at = rows[4 * m + g][q];
+      const int64_t at = rows[16 * m + 4 * g + q];
       const f32x4 d = {acc[m][0][q], acc[m][1][q], acc[m][2][q], acc[m][3][q]};
-      if (at >= 0) store_y<BF16, VECY>(p.y, size_t(at) * p.N + n, n, p.N, as_f32(yv[m][q]) + d);
+      if (at >= 0) store_y<BF16, VECY>(p.y, size_t(at) + n, n, p.N, as_f32(yv[m][q]) + d);
     }
 }
 
-// The rows of a tile, in LDS: kept in registers, they and the addresses made of
-// them take the 40 that a workgroup of 16 waves does not have.
+// Where the rows of a tile begin in y, in elements, or -1; in LDS: in registers they
+// and the addresses made of them take the 40 that a workgroup of 16 waves does not
+// have.
 template <int MS>
-__device__ __forceinline__ void put_rows(const LoraProblem& p, const Tile& t, i32x4* rows) {
-  if (threadIdx.x < MS * 16) reinterpret_cast<int*>(rows)[threadIdx.x] = row_at(p, t, threadIdx.x);
+__device__ __forceinline__ void put_rows(const LoraProblem& p, const Tile& t, int64_t* rows) {
+  if (threadIdx.x < MS * 16) {
+    const int row = row_at(p, t, threadIdx.x);
+    rows[threadIdx.x] = row < 0 ? -1 : int64_t(row) * p.N;
+  }
 }
 
 template <int RP, int MS, bool BF16, bool VECB, bool VECY>
@@ -388,9 +412,9 @@ __global__ __launch_bounds__(kWaves * kWave) void k_lora_expand(LoraProblem p, i
   constexpr int kThreads = kWaves * kWave;
   constexpr int kItems = MS * 16 * RP / 4;               // four ranks of a row
   constexpr int kEach = (kItems + kThreads - 1) / kThreads;
-  __shared__ __attribute__((aligned(16))) uint16_t ts[MS * 16 * P::LD];
+  __shared__ __attribute__((aligned(16))) char ts[MS * P::kT];
   __shared__ __attribute__((aligned(16))) char bstage[kWaves * P::kB];
-  __shared__ i32x4 rows[MS * 4];
+  __shared__ __attribute__((aligned(16))) int64_t rows[MS * 16];
   Tile t;
   if (!find_tile(p.offsets, p.S, 16 * MS, blockIdx.x, t)) return;
   const int wave = threadIdx.x >> 6;
@@ -423,7 +447,7 @@ __global__ __launch_bounds__(kWaves * kWave) void k_lora_expand(LoraProblem p, i
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int it = threadIdx.x + kThreads * i;
-    if (it < kItems) put_t<RP>(ts + it / (RP / 4) * P::LD, 4 * (it % (RP / 4)), p.r, scale, sum[i]);
+    if (it < kItems) put_t<RP>(ts, it / (RP / 4), 4 * (it % (RP / 4)), p.r, scale, sum[i]);
   }
   clear_tail<RP, MS>(ts, threadIdx.x, kThreads);
   put_rows<MS>(p, t, rows);
@@ -450,8 +474,8 @@ struct FusedLds {
   static constexpr int kB = Parts<RP>::kB;
   static constexpr int kMost = kStage > kRed ? kStage : kRed;
   static constexpr int kWork = kFusedWaves * (kMost > kB ? kMost : kB);
-  static constexpr int kRows = kWork + MS * 16 * Parts<RP>::LD * 2;
-  static constexpr int kBytes = kRows + MS * 16 * 4;
+  static constexpr int kRows = kWork + MS * Parts<RP>::kT;
+  static constexpr int kBytes = kRows + MS * 16 * 8;
 };
 
 template <int RP, int MS, bool BF16, bool VECB, bool VECY>
@@ -460,8 +484,8 @@ __global__ __launch_bounds__(kFusedWaves * kWave) void k_lora_fused(LoraProblem 
   using L = FusedLds<RP, MS>;
   constexpr int NR = L::NR;
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  uint16_t* ts = reinterpret_cast<uint16_t*>(smem + L::kWork);
-  i32x4* rows = reinterpret_cast<i32x4*>(smem + L::kRows);
+  char* ts = smem + L::kWork;
+  int64_t* rows = reinterpret_cast<int64_t*>(smem + L::kRows);
   Tile t;
   if (!find_tile(p.offsets, p.S, 16 * MS, blockIdx.x, t)) return;
   const int lane = lane_id(), wave = threadIdx.x >> 6;
@@ -493,16 +517,16 @@ __global__ __launch_bounds__(kFusedWaves * kWave) void k_lora_fused(LoraProblem 
     for (int w = 1; w < kFusedWaves; ++w) v += red[w * MS * NR * kWave + it];
     const int mj = it / kWave, l = it % kWave;
     const int j = 16 * (mj % NR) + 4 * (l >> 4);
-    if (j < RP) put_t<RP>(ts + (16 * (mj / NR) + (l & 15)) * P::LD, j, p.r, scale, v);
+    if (j < RP) put_t<RP>(ts, 16 * (mj / NR) + (l & 15), j, p.r, scale, v);
   }
   __syncthreads();
   char* bs = smem + wave * P::kB;                // and B's rows after that
   while (n0 < n1) {
     if (!kAhead) load_b<RP, VECB>(p, t, n0, bv);
-    put_b<RP, VECB>(p, t, n0, bs, bv);
-    __builtin_amdgcn_sched_barrier(0);           // the steps as they stand: 128 registers
     RawY<BF16> yv[MS][4];
     load_cols<MS, BF16, VECY>(p, n0, rows, yv);
+    __builtin_amdgcn_sched_barrier(0);           // the steps as they stand: 128 registers
+    put_b<RP, VECB>(p, t, n0, bs, bv);
     __builtin_amdgcn_sched_barrier(0);
     const int n = n0;
     n0 += kFusedWaves * kCols;
