@@ -549,11 +549,13 @@ size_t lora_add_workspace_bytes(int M, int K, int N, int S, int r);
  *   y           [M, N] f32 or bf16 (y_dtype), read and written; aligned to its
  *               elements
  *   workspace   lora_add_workspace_bytes(M, K, N, S, r) bytes, 16-byte
- *               aligned; its contents need no initialisation.  Calls that
- *               share one must not overlap
+ *               aligned (may be NULL when that is 0); its contents need no
+ *               initialisation.  Calls that share one must not overlap
  * Products are exact and sums, the scaled a x among them, are fp32; a bf16 y
- * is rounded once (RNE).  Deterministic.  K a multiple of 8 up to 2^17, N up to
- * 2^17, M up to 2^20, S up to 1024, r up to 128; x, a and b 16-byte aligned.
+ * is rounded once (RNE).  What is infinite or NaN in a row of x, a or y stays in
+ * the rows that read it; b is taken to be finite.  Deterministic.  K a multiple
+ * of 8 up to 2^17, N up to 2^17, M up to 2^20, S up to 1024, r up to 128; x, a and
+ * b 16-byte aligned.
  * Not on the pages: serving many fine-tuned variants of one set of weights.
  */
 int lora_add(const uint16_t* x_bf16, const int32_t* sorted_rows, const int32_t* offsets, int M,

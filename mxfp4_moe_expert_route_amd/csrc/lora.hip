@@ -2,12 +2,17 @@
 //
 // Rows come grouped by adapter (the lists of moe_permute), so a tile of rows
 // has one adapter and both steps are small matrix products on
-// v_mfma_f32_16x16x32_bf16.
+// v_mfma_f32_16x16x32_bf16.  Operations are few (2 r (K + N) a row); what counts is
+// the bytes of x and y for many rows, of A and B for few, and for the smallest calls
+// the launch.  8 rows of K = 6144, N = 4096, rank 16: 8.8 us, a launch and a chain of
+// four loads; 8192 rows of rank 64: 50 us where the caches hold x and y, 70 (3.4 TB/s)
+// where they do not.
 #include "lora.hpp"
 
 namespace mxm {
 namespace {
 
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 typedef __attribute__((ext_vector_type(2))) float f32x2;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2v;
@@ -18,18 +23,42 @@ constexpr int kCols = 64;            // columns of y a wave holds at a time
 // rank padded to a size that the kernels are made for
 int padded(int r) { return r <= 8 ? 8 : r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 
-// row tiles of 16 a workgroup takes: two where that leaves a workgroup for every CU
-int tile_rows(const LoraProblem& p) {
-  const int mean = p.M / (p.M < p.S ? p.M : p.S);
-  return mean >= 32 && p.M >= 4096 ? 2 : 1;
-}
-
 int64_t most_tiles(const LoraProblem& p, int mt) {
   const int64_t n = p.M / mt + int64_t(p.S);
   return n < p.M ? n : p.M;
 }
 
-// pieces of K, one workgroup each
+// Ranges of columns for the kernel that takes both steps: one round of workgroups,
+// those without rows too, which take a CU until they know it.  2048 rows of K = 6144
+// in one range 20.7 us, in two (272 workgroups) 17.1; 512 rows of 32 adapters in
+// four ranges (256) 10.3, in five 15.6.
+constexpr int kRound = 288;
+int col_ranges(const LoraProblem& p, int ms) {
+  const int64_t tiles = most_tiles(p, 16 * ms), cols = (p.N + kCols - 1) / kCols;
+  int64_t ranges = (255 + tiles) / tiles;
+  if (ranges > 1 && tiles * ranges > kRound) --ranges;
+  return int(ranges < cols ? ranges : cols);
+}
+
+int padded_tiles(int r) { return (padded(r) + 15) / 16; }
+
+// Row tiles of 16 a workgroup takes: two where that costs less, a workgroup's time
+// being taken as the tiles of x and A it reads and, in their measure, its part of
+// y.  In us, one and two: 8192 rows of K = 6144, N = 4096, rank 64 91 and 69; 4096
+// rows of 32 adapters, rank 32, fp32 51 and 57.
+int tile_rows(const LoraProblem& p) {
+  const int groups = p.M < p.S ? p.M : p.S;
+  if (p.M / groups < 32) return 1;
+  double cost[2];
+  for (int ms = 1; ms <= 2; ++ms) {
+    const int64_t tiles = p.M / (16 * ms) + groups / 2;     // an adapter's last tile half full
+    const int64_t rounds = (tiles + kRound - 1) / kRound;
+    cost[ms - 1] = double(rounds) * (ms + padded_tiles(p.r) + ms * 2.0 * p.N / p.K / col_ranges(p, ms));
+  }
+  return cost[1] < cost[0] ? 2 : 1;
+}
+
+// pieces of K, one workgroup each, until there are two for every CU
 int k_splits(const LoraProblem& p) {
   const int64_t tiles = most_tiles(p, 16 * tile_rows(p));
   int n = 1;
@@ -54,7 +83,8 @@ __device__ __forceinline__ int row_at(const LoraProblem& p, const Tile& t, int i
 // in the operands' order, a row a lane, the vector cache gives less than half of
 // that rate (8.4 of 18.5 TB/s where it hits L2).  So each 1 KB block goes through
 // `stage`, (MS + NR) KB of LDS that no other wave touches: piece q of row i at
-// 256 q + 16 (i ^ 4 q), which both sides reach without bank conflicts.  Of an
+// 256 q + 16 (i ^ 4 q), so that sixteen lanes read one window of 256 bytes and
+// sixteen lanes write to sixteen different bank groups.  Of an
 // operand lane 16 g + i holds row i (of A: operand A, of x: operand B), K 8 g ..
 // 8 g + 7; lane 16 g + c of the result holds ranks 4 g .. 4 g + 3 of row c.  Rows
 // past the tile and ranks past the last repeat others and are not used.
@@ -155,58 +185,68 @@ __global__ __launch_bounds__(kWaves * kWave) void k_lora_shrink(LoraProblem p, i
 
 // Four neighbouring elements of y as they lie in memory.
 template <bool BF16>
-using RawY = std::conditional_t<BF16, uint2, f32x4>;
+using RawY = std::conditional_t<BF16, u32x2, f32x4>;
 
-// columns past the last repeat it, and are not stored
+// Columns past the last repeat it, and are not stored.  Loads and stores with the
+// non-temporal hint are faster for a y that no cache holds (8192 rows of rank 16 48
+// us, 54 without) and slower for one that the projection has just written, which
+// the memory-side cache holds (44 against 40, N = 6144 56 against 42): no hint.
 template <bool BF16, bool VEC>
 __device__ __forceinline__ RawY<BF16> load_y(const void* y, size_t at, int n, int N) {
   if constexpr (VEC) {
     n = min(n, N - 4);                           // N is a multiple of 4
+    const RawY<BF16>* q;
     if constexpr (BF16) {
-      return *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(y) + at + n);
+      q = reinterpret_cast<const RawY<BF16>*>(static_cast<const uint16_t*>(y) + at + n);
     } else {
-      return *reinterpret_cast<const f32x4*>(static_cast<const float*>(y) + at + n);
+      q = reinterpret_cast<const RawY<BF16>*>(static_cast<const float*>(y) + at + n);
     }
+    return *q;
   } else if constexpr (BF16) {
     const uint16_t* q = static_cast<const uint16_t*>(y) + at;
     const uint32_t v0 = q[min(n, N - 1)], v1 = q[min(n + 1, N - 1)], v2 = q[min(n + 2, N - 1)], v3 = q[min(n + 3, N - 1)];
-    return make_uint2(v0 | v1 << 16, v2 | v3 << 16);
+    return u32x2{v0 | v1 << 16, v2 | v3 << 16};
   } else {
     const float* q = static_cast<const float*>(y) + at;
     return f32x4{q[min(n, N - 1)], q[min(n + 1, N - 1)], q[min(n + 2, N - 1)], q[min(n + 3, N - 1)]};
   }
 }
 
-__device__ __forceinline__ f32x4 as_f32(uint2 u) {
-  return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-               __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)};
+__device__ __forceinline__ f32x4 as_f32(u32x2 u) {
+  return f32x4{__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xffff0000u),
+               __uint_as_float(u[1] << 16), __uint_as_float(u[1] & 0xffff0000u)};
 }
 __device__ __forceinline__ f32x4 as_f32(f32x4 v) { return v; }
 
 template <bool BF16, bool VEC>
 __device__ __forceinline__ void store_y(void* y, size_t at, int n, int N, f32x4 v) {
+  RawY<BF16> u;
   if constexpr (BF16) {
-    uint16_t* q = static_cast<uint16_t*>(y) + at;
     const bf16x2v lo = __builtin_convertvector(f32x2{v[0], v[1]}, bf16x2v);      // to nearest even
     const bf16x2v hi = __builtin_convertvector(f32x2{v[2], v[3]}, bf16x2v);
-    const uint2 u = make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
-    if constexpr (VEC) {
-      if (n < N) *reinterpret_cast<uint2*>(q) = u;
+    u = u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+  } else {
+    u = v;
+  }
+  if constexpr (VEC) {
+    if (n >= N) return;
+    RawY<BF16>* q;
+    if constexpr (BF16) {
+      q = reinterpret_cast<RawY<BF16>*>(static_cast<uint16_t*>(y) + at);
     } else {
-      const uint32_t h[4] = {u.x & 0xffffu, u.x >> 16, u.y & 0xffffu, u.y >> 16};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < N) q[i] = uint16_t(h[i]);
+      q = reinterpret_cast<RawY<BF16>*>(static_cast<float*>(y) + at);
     }
+    *q = u;
+  } else if constexpr (BF16) {
+    uint16_t* q = static_cast<uint16_t*>(y) + at;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < N) q[i] = uint16_t(u[i >> 1] >> 16 * (i & 1));
   } else {
     float* q = static_cast<float*>(y) + at;
-    if constexpr (VEC) {
-      if (n < N) *reinterpret_cast<f32x4*>(q) = v;
-    } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < N) q[i] = v[i];
-    }
+    for (int i = 0; i < 4; ++i)
+      if (n + i < N) q[i] = u[i];
   }
 }
 
@@ -574,12 +614,7 @@ template <int RP, int MS>
 hipError_t launch_fused(const LoraProblem& p, hipStream_t s) {
   const unsigned tiles = unsigned(most_tiles(p, 16 * MS));
   const unsigned cols = unsigned((p.N + kCols - 1) / kCols);
-  // One round of workgroups, those without rows too, which take a CU until they
-  // know it: 2048 rows of K = 6144 in one range of columns 20.7 us, in two (272
-  // workgroups) 17.1; 512 rows of 32 adapters in four ranges (256) 10.3, in five 15.6.
-  unsigned ranges = (255 + tiles) / tiles;
-  if (ranges > 1 && tiles * ranges > 288) --ranges;
-  ranges = ranges < cols ? ranges : cols;
+  const unsigned ranges = unsigned(col_ranges(p, MS));
   const int chunks = int((cols + ranges - 1) / ranges);
   const dim3 grid(tiles, (cols + chunks - 1) / chunks);
   hipError_t e = hipSuccess;
@@ -598,9 +633,12 @@ hipError_t launch_fused(const LoraProblem& p, hipStream_t s) {
 
 // One launch wherever it is not much slower: a workgroup reads (ms + nr) 32 K bytes
 // for its t, at 60 to 80 GB/s, and every range of columns reads them again.  With
-// a workgroup for nearly every CU from the row tiles alone there is one range.
+// a workgroup for nearly every CU from the row tiles alone there is one range.  In
+// us, one launch and two, of which the second costs the caller 3 more: 8 rows of K =
+// 6144, N = 4096, rank 16 9.1 and 7.3; of N = 6144, rank 64 18 and 8.7; 8192 rows of
+// rank 64 50 and 59.
 bool fused(const LoraProblem& p) {
-  const int ms = tile_rows(p), nr = (padded(p.r) + 15) / 16;
+  const int ms = tile_rows(p), nr = padded_tiles(p.r);
   if (nr > 4) return false;
   return int64_t(ms + nr) * 32 * p.K <= 512 * 1024 || p.M / (16 * ms) >= 192;
 }

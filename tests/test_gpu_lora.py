@@ -217,6 +217,66 @@ def test_workspace_streams_replays_and_refusals(mm):
     assert empty.shape == (0, yt.shape[1])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_zero_adapters_keep_every_value(mm, dtype):
+    """y + 0 is y, for the smallest and largest numbers of its type too."""
+    say("lora_add of nothing", dtype)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    bits = torch.int16 if dtype == torch.bfloat16 else torch.int32
+    top = 0x7f80 if dtype == torch.bfloat16 else 0x7f800000
+    for M, r in ((40, 16), (40, 100)):
+        mag = torch.randint(0, top, (M, 96), device=DEV, generator=g)      # every finite magnitude
+        mag[:, :48] = mag[:, :48] >> 8                                      # half of them tiny or subnormal
+        sign = torch.where(torch.rand(M, 96, device=DEV, generator=g) < 0.5, -1, 1).to(dtype)
+        y = mag.to(bits).view(dtype) * sign
+        before = y.clone()
+        x = torch.randn(M, 64, device=DEV, generator=g).bfloat16()
+        a, b = torch.zeros(2, r, 64, dtype=torch.bfloat16, device=DEV), torch.ones(2, 96, r, dtype=torch.bfloat16, device=DEV)
+        mm.lora_add(x, *lists(mm, np.arange(M) % 2, 2), a, b, y)
+        assert torch.equal(y, before)
+
+
+def test_more_than_2_to_32_elements_of_y(mm):
+    say("lora_add past 32 bits")
+    M, K, N, S, r = 270000, 8, 16384, 2, 8
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x = torch.randint(-2, 3, (M, K), device=DEV, generator=g).bfloat16()
+    a = torch.randint(-2, 3, (S, r, K), device=DEV, generator=g).bfloat16()
+    b = torch.randint(-2, 3, (S, N, r), device=DEV, generator=g).bfloat16()
+    y = torch.zeros(M, N, dtype=torch.bfloat16, device=DEV)
+    assert y.numel() > 2 ** 32
+    slots = torch.randint(-1, S, (M, 1), device=DEV, generator=g).int()
+    _, offsets, rows, _ = mm.moe_permute(slots, S)
+    mm.lora_add(x, rows, offsets, a, b, y)
+    for m in (0, 1, 131071, 131072, 262143, 262144, M - 2, M - 1):
+        s = int(slots[m])
+        want = torch.zeros(N, device=DEV) if s < 0 else b[s].float() @ (a[s].float() @ x[m].float())
+        assert torch.equal(y[m], want.bfloat16()), m
+
+
+def test_two_calls_at_once(mm):
+    """Two streams, a workspace each, the same inputs."""
+    say("lora_add on two streams")
+    rng = np.random.default_rng(10)
+    M, K, N, S, r = 96, 1024, 640, 3, 100
+    x, a, b, y, scale = inputs(rng, M, K, N, S, r, False)
+    (xt, _), (at, _), (bt, _), (yt, _) = bf16(x), bf16(a), bf16(b), store(y, torch.bfloat16)
+    ll = lists(mm, rng.integers(-1, S, M), S)
+    want = mm.lora_add(xt, *ll, at, bt, yt.clone())
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    nws = mm.lora_add_workspace_bytes(M, K, N, S, r)
+    assert nws > 0
+    ws = [torch.empty(nws, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    outs = [[yt.clone() for _ in range(8)] for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for j, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                mm.lora_add(xt, *ll, at, bt, outs[j][i], workspace=ws[j])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for side in outs for o in side)
+
+
 def test_projection_router_and_routing_together(mm):
     """Rows of several requests: the shared product in MXFP4, the adapters beside it, the
     adapted router's logits, and the experts of each token from them."""
