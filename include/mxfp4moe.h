@@ -490,7 +490,7 @@ int dflash_verify_probs(const void* target_probs, const void* draft_probs, int d
  * Values c are compared in fp64 (a group's sum, too); one that lies within
  * fp64's rounding of another may be taken for equal or for the other side.
  * Renormalised weights hold where every chosen score underflows.  Weights are
- * within 2^-21 of the rule's, relative (below fp32's normal range 2^-149,
+ * within 2^-18 of the rule's, relative (below fp32's normal range 2^-148,
  * absolute).  Deterministic.  1 <= k <= min(32, topk_groups E/groups),
  * E <= 1024; an unknown score is MXM_ERR_DTYPE, all else MXM_ERR_SHAPE.
  * The pages give 384 experts with 8 active per token and no scoring rule; these

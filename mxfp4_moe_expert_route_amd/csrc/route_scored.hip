@@ -154,6 +154,15 @@ __device__ __forceinline__ void score_rows(const float* __restrict__ logits,
     }
     total = row_sum_f32(sum);
     const float inv = __builtin_amdgcn_rcpf(total);
+    if (!r.norm) {                               // the weights' divisor, more exactly
+      float more = 0.f;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const float e = exp_down(v[i] == top ? 0.0 : double(v[i]) - double(top));
+        more += v[i] > none ? e : 0.f;
+      }
+      total = row_sum_f32(more);
+    }
     ds = 0x1p-18f * inv;
 #pragma unroll
     for (int i = 0; i < NP; ++i) c[i] *= inv;

@@ -19,8 +19,9 @@
 // fp32 values, orders them by their differences (order_of), which do not lose
 // what the values lose, and keeps the first k if the last of them is further
 // above whatever is no candidate than the values' errors; otherwise it chooses
-// again in fp64.  8192 tokens of 384 experts in 8 groups: 12 us, 36 in fp64
-// throughout; a choice in fp64 at the end of a launch costs it 3.
+// again in fp64.  8192 tokens of 384 experts in 8 groups: 12 us a wave a token, 10
+// four tokens a wave (route_scored.hip), 36 in fp64 throughout; what bounds it are
+// a wave's instructions, and a choice in fp64 at the end of a launch costs it 3.
 #pragma once
 #include "routing.hpp"
 
@@ -296,9 +297,10 @@ __device__ __forceinline__ int order_of(float l, float b, int id, float s, float
   float ds = (up ? s : ns) * t;
   if (sigmoid) ds *= up ? nu : u;
   const float db = b - nb;
-  // values that fp64 does not tell apart are equal: left to it
+  // values that fp64 does not tell apart are equal: left to it, as are scores that
+  // fp32 holds with few digits
   const float err = (sigmoid ? 0x1p-20f : 0x1p-17f) * ds + 0x1p-22f * fabsf(db) +
-                    0x1p-51f * (fabsf(s) + fabsf(b));
+                    0x1p-51f * (fabsf(s) + fabsf(b)) + 0x1p-140f;
   const float x = (up ? ds : -ds) + db;
   if (l == nl && b == nb) return by_id;
   return x > err ? 1 : x < -err ? -1 : 0;
