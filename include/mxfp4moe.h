@@ -490,8 +490,8 @@ int dflash_verify_probs(const void* target_probs, const void* draft_probs, int d
  * Values c are compared in fp64 (a group's sum, too); one that lies within
  * fp64's rounding of another may be taken for equal or for the other side.
  * Renormalised weights hold where every chosen score underflows.  Weights are
- * within 2^-18 of the rule's, relative (below fp32's normal range 2^-148,
- * absolute).  Deterministic.  1 <= k <= min(32, topk_groups E/groups),
+ * within 2^-18 of the rule's, relative (below fp32's normal range, before the
+ * factor, 2^-148 times it).  Deterministic.  1 <= k <= min(32, topk_groups E/groups),
  * E <= 1024; an unknown score is MXM_ERR_DTYPE, all else MXM_ERR_SHAPE.
  * The pages give 384 experts with 8 active per token and no scoring rule; these
  * are the rules of layers that balance experts by a bias or keep tokens to a
@@ -552,10 +552,10 @@ size_t lora_add_workspace_bytes(int M, int K, int N, int S, int r);
  *               aligned (may be NULL when that is 0); its contents need no
  *               initialisation.  Calls that share one must not overlap
  * Products are exact and sums, the scaled a x among them, are fp32; a bf16 y
- * is rounded once (RNE).  What is infinite or NaN in a row of x, a or y stays in
- * the rows that read it; b is taken to be finite.  Deterministic.  K a multiple
- * of 8 up to 2^17, N up to 2^17, M up to 2^20, S up to 1024, r up to 128; x, a and
- * b 16-byte aligned.
+ * is rounded once (RNE).  y overlaps no input.  What is infinite or NaN in a row
+ * of x, a or y stays in the rows that read it; b is taken to be finite.
+ * Deterministic.  K a multiple of 8 up to 2^17, N up to 2^17, M up to 2^20, S up
+ * to 1024, r up to 128; x, a and b 16-byte aligned.
  * Not on the pages: serving many fine-tuned variants of one set of weights.
  */
 int lora_add(const uint16_t* x_bf16, const int32_t* sorted_rows, const int32_t* offsets, int M,

@@ -23,44 +23,48 @@ constexpr int kCols = 64;            // columns of y a wave holds at a time
 // rank padded to a size that the kernels are made for
 int padded(int r) { return r <= 8 ? 8 : r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 
-int64_t most_tiles(const LoraProblem& p, int mt) {
-  const int64_t n = p.M / mt + int64_t(p.S);
+int64_t most_tiles(const LoraProblem& p, int rows) {
+  const int64_t n = p.M / rows + int64_t(p.S);
   return n < p.M ? n : p.M;
-}
-
-// Ranges of columns for the kernel that takes both steps: one round of workgroups,
-// those without rows too, which take a CU until they know it.  2048 rows of K = 6144
-// in one range 20.7 us, in two (272 workgroups) 17.1; 512 rows of 32 adapters in
-// four ranges (256) 10.3, in five 15.6.
-constexpr int kRound = 288;
-int col_ranges(const LoraProblem& p, int ms) {
-  const int64_t tiles = most_tiles(p, 16 * ms), cols = (p.N + kCols - 1) / kCols;
-  int64_t ranges = (255 + tiles) / tiles;
-  if (ranges > 1 && tiles * ranges > kRound) --ranges;
-  return int(ranges < cols ? ranges : cols);
 }
 
 int padded_tiles(int r) { return (padded(r) + 15) / 16; }
 
-// Row tiles of 16 a workgroup takes: two where that costs less, a workgroup's time
-// being taken as the tiles of x and A it reads and, in their measure, its part of
-// y.  In us, one and two: 8192 rows of K = 6144, N = 4096, rank 64 91 and 69; 4096
-// rows of 32 adapters, rank 32, fp32 51 and 57.
-int tile_rows(const LoraProblem& p) {
-  const int groups = p.M < p.S ? p.M : p.S;
-  if (p.M / groups < 32) return 1;
-  double cost[2];
-  for (int ms = 1; ms <= 2; ++ms) {
-    const int64_t tiles = p.M / (16 * ms) + groups / 2;     // an adapter's last tile half full
-    const int64_t rounds = (tiles + kRound - 1) / kRound;
-    cost[ms - 1] = double(rounds) * (ms + padded_tiles(p.r) + ms * 2.0 * p.N / p.K / col_ranges(p, ms));
+// Rows of a tile for the kernel that takes both steps, whose workgroups have a CU to
+// themselves: as few as fill the chip once, or twice, ..., where every adapter's
+// last tile may be nearly empty, and 48 at most; or 16, where fewer would do.  A
+// tile more than the chip holds costs another round: 8192 rows of 8 adapters by
+// chance, rank 64, tiles of 32 rows 106 us, of 34 FIGURE.
+constexpr int kCus = 256;
+constexpr int kMostRows = 48;
+int fused_rows(const LoraProblem& p, int* holds = nullptr) {
+  const int64_t groups = p.M < p.S ? p.M : p.S;
+  for (int places = kCus;; places += kCus) {
+    if (places <= groups) continue;
+    const int64_t rows = (p.M + places - groups - 1) / (places - groups);
+    if (rows > kMostRows) continue;
+    if (holds) *holds = places;
+    return rows < 16 ? 16 : int(rows);
   }
-  return cost[1] < cost[0] ? 2 : 1;
 }
+
+// Ranges of columns for it: one round of workgroups, those without rows too, which
+// take a CU until they know it.  2048 rows of K = 6144 in one range 20.7 us, in two
+// (272 workgroups) 17.1; 512 rows of 32 adapters in four ranges (256) 10.3, in five
+// 15.6.
+int col_ranges(const LoraProblem& p, int rows) {
+  const int64_t tiles = most_tiles(p, rows), cols = (p.N + kCols - 1) / kCols;
+  int64_t ranges = (kCus - 1 + tiles) / tiles;
+  if (ranges > 1 && tiles * ranges > kCus + 32) --ranges;
+  return int(ranges < cols ? ranges : cols);
+}
+
+// Rows of a tile for the two kernels of a step each.
+int step_rows(const LoraProblem& p) { return p.M >= 32 * (p.M < p.S ? p.M : p.S) ? 32 : 16; }
 
 // pieces of K, one workgroup each, until there are two for every CU
 int k_splits(const LoraProblem& p) {
-  const int64_t tiles = most_tiles(p, 16 * tile_rows(p));
+  const int64_t tiles = most_tiles(p, step_rows(p));
   int n = 1;
   while (n < 16 && tiles * n < 512 && p.K >= 2 * n * 256) n *= 2;
   return n;
@@ -88,18 +92,19 @@ __device__ __forceinline__ int row_at(const LoraProblem& p, const Tile& t, int i
 // operand lane 16 g + i holds row i (of A: operand A, of x: operand B), K 8 g ..
 // 8 g + 7; lane 16 g + c of the result holds ranks 4 g .. 4 g + 3 of row c.  Rows
 // past the tile and ranks past the last repeat others and are not used.
-template <int NR, int MS>
+template <int NR, int MS, bool Few = false>
 __device__ __forceinline__ void shrink_part(const LoraProblem& p, const Tile& t, int k0, int k1,
                                             int stride, char* stage, f32x4 (&acc)[MS][NR]) {
   constexpr int R = MS + NR;
-  constexpr int U = R <= 2 ? 6 : R <= 3 ? 4 : R <= 5 ? 3 : 2;     // steps whose loads go out together
+  // steps whose loads go out together: more, where few waves have the registers
+  constexpr int U = Few ? 4 : R <= 2 ? 6 : R <= 3 ? 4 : R <= 5 ? 3 : 2;
   const int lane = lane_id();
   const int lr = lane >> 2, lp = lane & 3;       // loading: row and piece
   const int c = lane & 15, g = lane >> 4;
   const uint16_t* src[R];
 #pragma unroll
   for (int m = 0; m < MS; ++m)
-    src[m] = p.x + size_t(max(row_at(p, t, 16 * m + lr), 0)) * p.K;
+    src[m] = p.x + size_t(max(row_at(p, t, min(16 * m + lr, t.rows - 1)), 0)) * p.K;
 #pragma unroll
   for (int j = 0; j < NR; ++j)
     src[MS + j] = p.a + (size_t(t.e) * p.r + min(16 * j + lr, p.r - 1)) * p.K;
@@ -393,7 +398,7 @@ __device__ __forceinline__ void load_cols(const LoraProblem& p, int n0, const in
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int64_t at = rows[16 * m + 4 * (lane >> 4) + q];
-      yv[m][q] = load_y<BF16, VECY>(p.y, size_t(at < 0 ? 0 : at), n, p.N);
+      yv[m][q] = load_y<BF16, VECY>(p.y, size_t(at < 0 ? ~at : at), n, p.N);
     }
 }
 
@@ -435,14 +440,17 @@ __device__ __forceinline__ void expand_cols(const LoraProblem& p, const char* ts
     }
 }
 
-// Where the rows of a tile begin in y, in elements, or -1; in LDS: in registers they
-// and the addresses made of them take the 40 that a workgroup of 16 waves does not
-// have.
+// Where the rows of a tile begin in y, in elements; for a place without a row, whose
+// values are loaded and not used, ~ that of the tile's last row.  In LDS: in registers
+// they and the addresses made of them take the 40 that a workgroup of 16 waves does
+// not have.
 template <int MS>
 __device__ __forceinline__ void put_rows(const LoraProblem& p, const Tile& t, int64_t* rows) {
-  if (threadIdx.x < MS * 16) {
-    const int row = row_at(p, t, threadIdx.x);
-    rows[threadIdx.x] = row < 0 ? -1 : int64_t(row) * p.N;
+  const int i = threadIdx.x;
+  if (i < MS * 16) {
+    const int row = row_at(p, t, min(i, t.rows - 1));
+    const int64_t at = int64_t(max(row, 0)) * p.N;
+    rows[i] = row < 0 || i >= t.rows ? ~at : at;
   }
 }
 
@@ -503,31 +511,30 @@ __global__ __launch_bounds__(kWaves * kWave) void k_lora_expand(LoraProblem p, i
   }
 }
 
-// Both steps of a tile in one workgroup of 16 waves, which computes t for itself:
-// one launch, no workspace, and t once for each of gridDim.y column ranges.
-constexpr int kFusedWaves = 16;
+// Both steps of a tile in one workgroup, which computes t for itself: one launch, no
+// workspace, and t once for each of gridDim.y column ranges.  16 waves; for three
+// row tiles, whose sums of 16 waves LDS does not hold, eight of twice the registers.
+template <int MS>
+constexpr int kFusedWaves = MS > 2 ? 8 : 16;
 
-template <int RP, int MS>
+template <int RP, int MS, int W>
 struct FusedLds {
   static constexpr int NR = (RP + 15) / 16;
   static constexpr int kStage = (MS + NR) * 1024, kRed = MS * NR * 1024;
   static constexpr int kB = Parts<RP>::kB;
   static constexpr int kMost = kStage > kRed ? kStage : kRed;
-  static constexpr int kWork = kFusedWaves * (kMost > kB ? kMost : kB);
+  static constexpr int kWork = W * (kMost > kB ? kMost : kB);
   static constexpr int kRows = kWork + MS * Parts<RP>::kT;
   static constexpr int kBytes = kRows + MS * 16 * 8;
 };
 
-template <int RP, int MS, bool BF16, bool VECB, bool VECY>
-__global__ __launch_bounds__(kFusedWaves * kWave) void k_lora_fused(LoraProblem p, int chunks) {
+template <int RP, int MS, int W, bool BF16, bool VECB, bool VECY>
+__device__ __forceinline__ void fused_tile(const LoraProblem& p, const Tile& t, int chunks, char* smem) {
   using P = Parts<RP>;
-  using L = FusedLds<RP, MS>;
+  using L = FusedLds<RP, MS, W>;
   constexpr int NR = L::NR;
-  extern __shared__ __attribute__((aligned(16))) char smem[];
   char* ts = smem + L::kWork;
   int64_t* rows = reinterpret_cast<int64_t*>(smem + L::kRows);
-  Tile t;
-  if (!find_tile(p.offsets, p.S, 16 * MS, blockIdx.x, t)) return;
   const int lane = lane_id(), wave = threadIdx.x >> 6;
   // column pieces blockIdx.y * chunks + wave, + 16, ...
   const int n1 = min(p.N, int(blockIdx.y + 1) * chunks * kCols);
@@ -538,8 +545,8 @@ __global__ __launch_bounds__(kFusedWaves * kWave) void k_lora_fused(LoraProblem 
   const float scale = p.scale ? p.scale[t.e] : 1.f;
   f32x4 acc[MS][NR];
   clear(acc);
-  shrink_part(p, t, 32 * wave, p.K, 32 * kFusedWaves, smem + wave * L::kStage, acc);
-  constexpr bool kAhead = RP * MS < 64;          // registers for the next of B meanwhile
+  shrink_part<NR, MS, W < 16>(p, t, 32 * wave, p.K, 32 * W, smem + wave * L::kStage, acc);
+  constexpr bool kAhead = W < 16 || RP * MS < 64;          // registers for the next of B meanwhile
   if (kAhead && !kEarly && n0 < n1) load_b<RP, VECB>(p, t, n0, bv);
   __syncthreads();                               // `red` lies where the stages were
   f32x4* red = reinterpret_cast<f32x4*>(smem);
@@ -547,14 +554,14 @@ __global__ __launch_bounds__(kFusedWaves * kWave) void k_lora_fused(LoraProblem 
   for (int m = 0; m < MS; ++m)
 #pragma unroll
     for (int j = 0; j < NR; ++j) red[(wave * MS * NR + m * NR + j) * kWave + lane] = acc[m][j];
-  clear_tail<RP, MS>(ts, threadIdx.x, kFusedWaves * kWave);
+  clear_tail<RP, MS>(ts, threadIdx.x, W * kWave);
   put_rows<MS>(p, t, rows);
   __syncthreads();
   // item (m, j, lane) as the waves hold it: ranks 16 j + 4 g .. + 3 of row 16 m + c
-  for (int it = threadIdx.x; it < MS * NR * kWave; it += kFusedWaves * kWave) {
+  for (int it = threadIdx.x; it < MS * NR * kWave; it += W * kWave) {
     f32x4 v = red[it];
 #pragma unroll
-    for (int w = 1; w < kFusedWaves; ++w) v += red[w * MS * NR * kWave + it];
+    for (int w = 1; w < W; ++w) v += red[w * MS * NR * kWave + it];
     const int mj = it / kWave, l = it % kWave;
     const int j = 16 * (mj % NR) + 4 * (l >> 4);
     if (j < RP) put_t<RP>(ts, 16 * (mj / NR) + (l & 15), j, p.r, scale, v);
@@ -569,10 +576,56 @@ __global__ __launch_bounds__(kFusedWaves * kWave) void k_lora_fused(LoraProblem 
     put_b<RP, VECB>(p, t, n0, bs, bv);
     __builtin_amdgcn_sched_barrier(0);
     const int n = n0;
-    n0 += kFusedWaves * kCols;
+    n0 += W * kCols;
     if (kAhead && n0 < n1) load_b<RP, VECB>(p, t, n0, bv);
     expand_cols<RP, MS, BF16, VECY>(p, ts, bs, n, rows, yv);
   }
+}
+
+constexpr int kChiplets = 8;
+
+// The tile of the b-th workgroup of one range of columns.  Tiles have `rows` rows, or a
+// row tile less than MS where as many rounds of `places` workgroups hold those.
+// Workgroups go to the eight chiplets in turn, each with a cache of its own: each
+// gets a run of neighbouring tiles, which share A_s and B_s (8192 rows of 32
+// adapters, 4096 of them 51 us without that and 47).
+template <int MS>
+__device__ __forceinline__ bool near_tile(const LoraProblem& p, int rows, int places, int b, Tile& t) {
+  const int lane = lane_id();
+  int tiles = 0, less = 0;
+  for (int c0 = 0; c0 < p.S; c0 += kWave) {
+    const int e = c0 + lane;
+    const int n = e < p.S ? p.offsets[e + 1] - p.offsets[e] : 0;
+    tiles += __builtin_amdgcn_readlane(wave_incl_scan((n + rows - 1) / rows), kWave - 1);
+    if constexpr (MS > 1)
+      less += __builtin_amdgcn_readlane(wave_incl_scan((n + 16 * (MS - 1) - 1) / (16 * (MS - 1))), kWave - 1);
+  }
+  if (MS > 1 && less <= places) {
+    tiles = less;
+    rows = 16 * (MS - 1);
+  }
+  const int x = b % kChiplets, each = tiles / kChiplets, left = tiles % kChiplets;
+  return b < tiles && find_tile(p.offsets, p.S, rows, x * each + min(x, left) + b / kChiplets, t);
+}
+
+template <int RP, int MS, bool BF16, bool VECB, bool VECY>
+__global__ __launch_bounds__(kFusedWaves<MS> * kWave) void k_lora_fused(LoraProblem p, int rows, int places,
+                                                                       int chunks) {
+  constexpr int W = kFusedWaves<MS>;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  Tile t;
+  if (gridDim.y == 1) {
+    if (!near_tile<MS>(p, rows, places, blockIdx.x, t)) return;
+  } else {
+    if (!find_tile(p.offsets, p.S, rows, blockIdx.x, t)) return;
+  }
+  if constexpr (MS > 1) {
+    if (t.rows <= 16 * (MS - 1)) {
+      fused_tile<RP, MS - 1, W, BF16, VECB, VECY>(p, t, chunks, smem);
+      return;
+    }
+  }
+  fused_tile<RP, MS, W, BF16, VECB, VECY>(p, t, chunks, smem);
 }
 
 // f(bf16, vector loads of B, vector accesses of y), as types
@@ -611,22 +664,24 @@ hipError_t launch_two(const LoraProblem& p, hipStream_t s) {
 }
 
 template <int RP, int MS>
-hipError_t launch_fused(const LoraProblem& p, hipStream_t s) {
-  const unsigned tiles = unsigned(most_tiles(p, 16 * MS));
+hipError_t launch_fused(const LoraProblem& p, int rows, int places, hipStream_t s) {
+  // or as many of a row tile less as `places` hold
+  const int64_t most = most_tiles(p, rows);
+  const unsigned tiles = unsigned(MS > 1 && most < places ? places : most);
   const unsigned cols = unsigned((p.N + kCols - 1) / kCols);
-  const unsigned ranges = unsigned(col_ranges(p, MS));
+  const unsigned ranges = unsigned(col_ranges(p, rows));
   const int chunks = int((cols + ranges - 1) / ranges);
   const dim3 grid(tiles, (cols + chunks - 1) / chunks);
   hipError_t e = hipSuccess;
   by_form(p, [&](auto bf, auto vecb, auto vecy) {
     const auto fn = &k_lora_fused<RP, MS, decltype(bf)::value, decltype(vecb)::value, decltype(vecy)::value>;
-    constexpr int lds = FusedLds<RP, MS>::kBytes;
+    constexpr int threads = kFusedWaves<MS> * kWave, lds = FusedLds<RP, MS, kFusedWaves<MS>>::kBytes;
     if (lds > 64 * 1024) {
       static std::atomic<bool> set[kMaxDevices];
       e = lds_limit_once(reinterpret_cast<const void*>(fn), lds, set);
       if (e != hipSuccess) return;
     }
-    fn<<<grid, kFusedWaves * kWave, lds, s>>>(p, chunks);
+    fn<<<grid, threads, lds, s>>>(p, rows, places, chunks);
   });
   return e != hipSuccess ? e : hipGetLastError();
 }
@@ -638,22 +693,23 @@ hipError_t launch_fused(const LoraProblem& p, hipStream_t s) {
 // 6144, N = 4096, rank 16 9.1 and 7.3; of N = 6144, rank 64 18 and 8.7; 8192 rows of
 // rank 64 50 and 59.
 bool fused(const LoraProblem& p) {
-  const int ms = tile_rows(p), nr = padded_tiles(p.r);
+  const int rows = fused_rows(p), ms = (rows + 15) / 16, nr = padded_tiles(p.r);
   if (nr > 4) return false;
-  return int64_t(ms + nr) * 32 * p.K <= 512 * 1024 || p.M / (16 * ms) >= 192;
-}
-
-template <int RP, int MS>
-hipError_t launch(const LoraProblem& p, hipStream_t s) {
-  if constexpr (RP <= 64) {
-    if (fused(p)) return launch_fused<RP, MS>(p, s);
-  }
-  return launch_two<RP, MS>(p, s);
+  return int64_t(ms + nr) * 32 * p.K <= 512 * 1024 || p.M / rows + (p.M < p.S ? p.M : p.S) / 2 >= 192;
 }
 
 template <int RP>
-hipError_t launch_r(const LoraProblem& p, hipStream_t s) {
-  return tile_rows(p) == 1 ? launch<RP, 1>(p, s) : launch<RP, 2>(p, s);
+hipError_t launch(const LoraProblem& p, hipStream_t s) {
+  if constexpr (RP <= 64) {
+    if (fused(p)) {
+      int places = 0;
+      const int rows = fused_rows(p, &places);
+      return rows <= 16 ? launch_fused<RP, 1>(p, rows, places, s)
+             : rows <= 32 ? launch_fused<RP, 2>(p, rows, places, s)
+                          : launch_fused<RP, 3>(p, rows, places, s);
+    }
+  }
+  return step_rows(p) == 16 ? launch_two<RP, 1>(p, s) : launch_two<RP, 2>(p, s);
 }
 
 }  // namespace
@@ -666,11 +722,11 @@ size_t lora_workspace_bytes(int M, int K, int N, int S, int r) {
 
 hipError_t launch_lora(const LoraProblem& p, hipStream_t s) {
   switch (padded(p.r)) {
-    case 8: return launch_r<8>(p, s);
-    case 16: return launch_r<16>(p, s);
-    case 32: return launch_r<32>(p, s);
-    case 64: return launch_r<64>(p, s);
-    default: return launch_r<128>(p, s);
+    case 8: return launch<8>(p, s);
+    case 16: return launch<16>(p, s);
+    case 32: return launch<32>(p, s);
+    case 64: return launch<64>(p, s);
+    default: return launch<128>(p, s);
   }
 }
 
