@@ -4,7 +4,7 @@
 // has one adapter and both steps are small matrix products on
 // v_mfma_f32_16x16x32_bf16.  Operations are few (2 r (K + N) a row); what counts is
 // the bytes of x and y for many rows, of A and B for few, and for the smallest calls
-// the launch.  8 rows of K = 6144, N = 4096, rank 16: 8.8 us, a launch and a chain of
+// the launch.  8 rows of K = 6144, N = 4096, rank 16: 8.6 us, a launch and a chain of
 // four loads; 8192 rows of rank 64: 50 us where the caches hold x and y, 70 (3.4 TB/s)
 // where they do not.
 #include "lora.hpp"
@@ -34,7 +34,7 @@ int padded_tiles(int r) { return (padded(r) + 15) / 16; }
 // themselves: as few as fill the chip once, or twice, ..., where every adapter's
 // last tile may be nearly empty, and 48 at most; or 16, where fewer would do.  A
 // tile more than the chip holds costs another round: 8192 rows of 8 adapters by
-// chance, rank 64, tiles of 32 rows 106 us, of 34 FIGURE.
+// chance, rank 64, tiles of 32 rows 106 us, of 34 75; of 64 adapters 126 and 82.
 constexpr int kCus = 256;
 constexpr int kMostRows = 48;
 int fused_rows(const LoraProblem& p, int* holds = nullptr) {
@@ -557,6 +557,11 @@ __device__ __forceinline__ void fused_tile(const LoraProblem& p, const Tile& t, 
   clear_tail<RP, MS>(ts, threadIdx.x, W * kWave);
   put_rows<MS>(p, t, rows);
   __syncthreads();
+  // The first of y meanwhile, and the next where there are registers for it: 8192 rows
+  // of rank 32, K = 2048, N = 6144 61 us without, 58 with.
+  constexpr bool kAheadY = VECY && W < 16 && RP * MS < (BF16 ? 192 : 128);
+  RawY<BF16> yv[MS][4];
+  if (VECY && n0 < n1) load_cols<MS, BF16, VECY>(p, n0, rows, yv);
   // item (m, j, lane) as the waves hold it: ranks 16 j + 4 g .. + 3 of row 16 m + c
   for (int it = threadIdx.x; it < MS * NR * kWave; it += W * kWave) {
     f32x4 v = red[it];
@@ -570,15 +575,26 @@ __device__ __forceinline__ void fused_tile(const LoraProblem& p, const Tile& t, 
   char* bs = smem + wave * P::kB;                // and B's rows after that
   while (n0 < n1) {
     if (!kAhead) load_b<RP, VECB>(p, t, n0, bv);
-    RawY<BF16> yv[MS][4];
-    load_cols<MS, BF16, VECY>(p, n0, rows, yv);
+    if (!VECY) load_cols<MS, BF16, VECY>(p, n0, rows, yv);
     __builtin_amdgcn_sched_barrier(0);           // the steps as they stand: 128 registers
     put_b<RP, VECB>(p, t, n0, bs, bv);
     __builtin_amdgcn_sched_barrier(0);
     const int n = n0;
     n0 += W * kCols;
     if (kAhead && n0 < n1) load_b<RP, VECB>(p, t, n0, bv);
-    expand_cols<RP, MS, BF16, VECY>(p, ts, bs, n, rows, yv);
+    if constexpr (kAheadY) {
+      RawY<BF16> next[MS][4];
+      if (n0 < n1) load_cols<MS, BF16, VECY>(p, n0, rows, next);
+      __builtin_amdgcn_sched_barrier(0);
+      expand_cols<RP, MS, BF16, VECY>(p, ts, bs, n, rows, yv);
+#pragma unroll
+      for (int m = 0; m < MS; ++m)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) yv[m][q] = next[m][q];
+    } else {
+      expand_cols<RP, MS, BF16, VECY>(p, ts, bs, n, rows, yv);
+      if (VECY && n0 < n1) load_cols<MS, BF16, VECY>(p, n0, rows, yv);
+    }
   }
 }
 
@@ -587,8 +603,8 @@ constexpr int kChiplets = 8;
 // The tile of the b-th workgroup of one range of columns.  Tiles have `rows` rows, or a
 // row tile less than MS where as many rounds of `places` workgroups hold those.
 // Workgroups go to the eight chiplets in turn, each with a cache of its own: each
-// gets a run of neighbouring tiles, which share A_s and B_s (8192 rows of 32
-// adapters, 4096 of them 51 us without that and 47).
+// gets a run of neighbouring tiles, which share A_s and B_s (4096 rows of 32
+// adapters, rank 32, fp32: 51 us without that, 47 with).
 template <int MS>
 __device__ __forceinline__ bool near_tile(const LoraProblem& p, int rows, int places, int b, Tile& t) {
   const int lane = lane_id();

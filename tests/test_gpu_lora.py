@@ -306,3 +306,21 @@ def test_projection_router_and_routing_together(mm):
     oid, ow = scored.route(logits.cpu().numpy(), 4, bias, groups=4, keep=2, scale=2.5)
     assert np.array_equal(ids.cpu().numpy(), oid)
     assert np.abs(wt.double().cpu().numpy() - ow).max() <= 2.0 ** -18 * 2.5
+
+
+# thousands of rows: tiles of 17 to 48 rows, of a multiple of 16 where those fit, one round and more
+HEIGHTS = [(4500, 72, 70, 3, 8), (6000, 40, 33, 20, 5), (8192, 64, 68, 8, 16), (8300, 40, 132, 5, 64), (12000, 48, 40, 60, 33),
+           (20000, 32, 36, 9, 30), (9000, 24, 64, 300, 16), (10100, 16, 4100, 3, 24)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", HEIGHTS, ids=lambda s: "x".join(map(str, s)))
+def test_tile_heights(mm, shape, dtype):
+    M, K, N, S, r = shape
+    say("lora_add tile heights", shape, dtype)
+    rng = np.random.default_rng(list(shape))
+    even = np.arange(M) * S // M
+    check(mm, even, K, N, S, r, dtype, True, rng)
+    check(mm, np.where(rng.random(M) < 0.02, -1, rng.integers(0, S, M)), K, N, S, r, dtype, True, rng)
+    check(mm, np.zeros(M, int), K, N, S, r, dtype, False, rng)
+    check(mm, np.minimum(rng.geometric(0.4, M) - 1, S - 1), K, N, S, r, dtype, False, rng)
