@@ -24,6 +24,7 @@ Modules
   route    top-k routing with softmax weights renormalised over the chosen k
   permute  per-expert histogram, offsets, gather lists
   layer    the whole layer by its plain per-expert dense definition
+  scored   routing by scores, a bias and groups; low-rank adapters
 
 Parity pins: every function here is pinned by tests under tests/ that check
 it against something other than itself (closed forms, the spec's bit-field
