@@ -74,6 +74,101 @@ __device__ __forceinline__ f32x4 mfma(uint4 a, uint4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
 }
 
+constexpr int kChiplets = 8;
+constexpr int kMostAdapters = 1024;
+
+// The tile of workgroup blockIdx.x, by all W waves of it; false if it has none.  Tiles
+// have `rows` rows; where there is one range of columns (near), a row tile less than MS
+// if as many rounds of `places` workgroups hold those.  Workgroups go to the eight
+// chiplets in turn, each with a cache of its own: each then gets a run of
+// neighbouring tiles, which share A_s and B_s (4096 rows of 32 adapters, rank 32,
+// fp32: 51 us without that, 47 with).  Up to 64 adapters every wave finds the tile
+// alone; of more each thread takes a few (512 rows of 1024 adapters, K = N = 2048: 33 us
+// 64 at a time in every wave, 18 so).
+template <int W, int MS>
+__device__ __forceinline__ bool place_tile(const LoraProblem& p, int rows, int places, bool near, Tile& t) {
+  constexpr int kEach = kMostAdapters / (W * kWave);
+  constexpr int kLess = MS > 1 ? 16 * (MS - 1) : 16;
+  __shared__ int32_t sums[2][W];
+  __shared__ int32_t found[3];
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  const bool alone = p.S <= kWave;
+  const int e0 = alone ? lane : int(threadIdx.x) * kEach;
+  int off[kEach], cnt[kEach], n = 0, l = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int e = e0 + i;
+    const bool in = e < p.S && (i == 0 || !alone);
+    off[i] = in ? p.offsets[e] : 0;
+    cnt[i] = in ? max(p.offsets[e + 1] - off[i], 0) : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    n += (cnt[i] + rows - 1) / rows;
+    l += (cnt[i] + kLess - 1) / kLess;
+  }
+  int n_to = wave_incl_scan(n), l_to = wave_incl_scan(l);
+  int tiles = __builtin_amdgcn_readlane(n_to, kWave - 1), less = __builtin_amdgcn_readlane(l_to, kWave - 1);
+  if (!alone) {
+    if (lane == kWave - 1) {
+      sums[0][wave] = n_to;
+      sums[1][wave] = l_to;
+    }
+    __syncthreads();
+    tiles = less = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w < wave) {
+        n_to += sums[0][w];
+        l_to += sums[1][w];
+      }
+      tiles += sums[0][w];
+      less += sums[1][w];
+    }
+  }
+  int first = n_to - n;
+  if (MS > 1 && near && less <= places) {
+    tiles = less;
+    rows = kLess;
+    first = l_to - l;
+  }
+  int at = blockIdx.x;
+  if (at >= tiles) return false;                 // the whole workgroup
+  if (near) {
+    const int x = at % kChiplets, left = tiles % kChiplets;
+    at = x * (tiles / kChiplets) + min(x, left) + at / kChiplets;
+  }
+  bool mine = false;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int k = (cnt[i] + rows - 1) / rows;
+    if (at >= first && at < first + k) {
+      mine = true;
+      t.e = e0 + i;
+      t.row0 = off[i] + (at - first) * rows;
+      t.rows = min(rows, cnt[i] - (at - first) * rows);
+    }
+    first += k;
+  }
+  if (alone) {
+    const int src = __ffsll((long long)__ballot(mine)) - 1;
+    t.e = __builtin_amdgcn_readlane(t.e, src);
+    t.row0 = __builtin_amdgcn_readlane(t.row0, src);
+    t.rows = __builtin_amdgcn_readlane(t.rows, src);
+    return true;
+  }
+  if (mine) {
+    found[0] = t.e;
+    found[1] = t.row0;
+    found[2] = t.rows;
+  }
+  __syncthreads();
+  t.e = __builtin_amdgcn_readfirstlane(found[0]);
+  t.row0 = __builtin_amdgcn_readfirstlane(found[1]);
+  t.rows = __builtin_amdgcn_readfirstlane(found[2]);
+  return true;
+}
+
 // The row of y and x at sorted position pos, or -1.
 __device__ __forceinline__ int row_at(const LoraProblem& p, const Tile& t, int i) {
   const int pos = t.row0 + i;
@@ -154,8 +249,8 @@ __global__ __launch_bounds__(kWaves * kWave) void k_lora_shrink(LoraProblem p, i
   constexpr int kStage = (MS + NR) * 1024, kRed = MS * NR * 1024;
   constexpr int kBytes = kWaves * kStage > (kWaves - 1) * kRed ? kWaves * kStage : (kWaves - 1) * kRed;
   __shared__ __attribute__((aligned(16))) char lds[kBytes];
-  Tile t;
-  if (!find_tile(p.offsets, p.S, 16 * MS, blockIdx.x, t)) return;
+  Tile t{};
+  if (!place_tile<kWaves, 1>(p, 16 * MS, 0, false, t)) return;
   const int lane = lane_id(), wave = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
   f32x4 acc[MS][NR];
@@ -463,8 +558,8 @@ __global__ __launch_bounds__(kWaves * kWave) void k_lora_expand(LoraProblem p, i
   __shared__ __attribute__((aligned(16))) char ts[MS * P::kT];
   __shared__ __attribute__((aligned(16))) char bstage[kWaves * P::kB];
   __shared__ __attribute__((aligned(16))) int64_t rows[MS * 16];
-  Tile t;
-  if (!find_tile(p.offsets, p.S, 16 * MS, blockIdx.x, t)) return;
+  Tile t{};
+  if (!place_tile<kWaves, 1>(p, 16 * MS, 0, false, t)) return;
   const int wave = threadIdx.x >> 6;
   const int step = gridDim.y * kWaves * kCols;
   int n0 = (blockIdx.y * kWaves + wave) * kCols;
@@ -598,43 +693,13 @@ __device__ __forceinline__ void fused_tile(const LoraProblem& p, const Tile& t, 
   }
 }
 
-constexpr int kChiplets = 8;
-
-// The tile of the b-th workgroup of one range of columns.  Tiles have `rows` rows, or a
-// row tile less than MS where as many rounds of `places` workgroups hold those.
-// Workgroups go to the eight chiplets in turn, each with a cache of its own: each
-// gets a run of neighbouring tiles, which share A_s and B_s (4096 rows of 32
-// adapters, rank 32, fp32: 51 us without that, 47 with).
-template <int MS>
-__device__ __forceinline__ bool near_tile(const LoraProblem& p, int rows, int places, int b, Tile& t) {
-  const int lane = lane_id();
-  int tiles = 0, less = 0;
-  for (int c0 = 0; c0 < p.S; c0 += kWave) {
-    const int e = c0 + lane;
-    const int n = e < p.S ? p.offsets[e + 1] - p.offsets[e] : 0;
-    tiles += __builtin_amdgcn_readlane(wave_incl_scan((n + rows - 1) / rows), kWave - 1);
-    if constexpr (MS > 1)
-      less += __builtin_amdgcn_readlane(wave_incl_scan((n + 16 * (MS - 1) - 1) / (16 * (MS - 1))), kWave - 1);
-  }
-  if (MS > 1 && less <= places) {
-    tiles = less;
-    rows = 16 * (MS - 1);
-  }
-  const int x = b % kChiplets, each = tiles / kChiplets, left = tiles % kChiplets;
-  return b < tiles && find_tile(p.offsets, p.S, rows, x * each + min(x, left) + b / kChiplets, t);
-}
-
 template <int RP, int MS, bool BF16, bool VECB, bool VECY>
 __global__ __launch_bounds__(kFusedWaves<MS> * kWave) void k_lora_fused(LoraProblem p, int rows, int places,
                                                                        int chunks) {
   constexpr int W = kFusedWaves<MS>;
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  Tile t;
-  if (gridDim.y == 1) {
-    if (!near_tile<MS>(p, rows, places, blockIdx.x, t)) return;
-  } else {
-    if (!find_tile(p.offsets, p.S, rows, blockIdx.x, t)) return;
-  }
+  Tile t{};
+  if (!place_tile<W, MS>(p, rows, places, gridDim.y == 1, t)) return;
   if constexpr (MS > 1) {
     if (t.rows <= 16 * (MS - 1)) {
       fused_tile<RP, MS - 1, W, BF16, VECB, VECY>(p, t, chunks, smem);
