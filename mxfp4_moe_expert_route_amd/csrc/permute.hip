@@ -109,28 +109,46 @@ __global__ __launch_bounds__(4 * kWave) void k_perm_scatter(const int32_t* __res
                    pair_to_row, smem, wave_sum);
 }
 
-// Up to kOneMaxPairs pairs of calls with k >= 4: every workgroup counts all pairs
-// for itself, those before its range apart, which gives it the offsets and its
-// bases without another launch (65536 pairs of 384 experts: 9 us, 17 in three
-// launches).  A token's pairs are of different experts, so with k >= 4 at most 16
-// of the 64 that a wave counts at a time meet on one counter.
-constexpr int kOneMaxPairs = 1 << 17;
+// One launch for calls with k >= 4 up to one_max_pairs(E) pairs: every workgroup
+// counts all pairs for itself, those before its range apart, which gives it the
+// offsets and its bases.  Lanes that meet on one counter take turns (two cycles a
+// lane), so there are eight copies of the counters: lanes of a run of eight have
+// one each, and so have eight lanes of those eight apart, whether a token's ids are
+// all the same or all tokens have the same ids.  In us, 65536 pairs of 384 experts,
+// so, with one copy and in three launches: distinct ids in each token 11.7, 12.9 and
+// 14.6; all ids the same 14.0, 61 and 15.3.
 constexpr int kOneWaves = 16;
 constexpr int kOneRange = 256;
 constexpr int kOneBatch = 16;                    // ids a thread loads together
+constexpr int kOneCopies = 8;
 
-// expert counters and bases, then permute_block's tables
-size_t one_lds(int E) { return size_t(2 + kOneWaves + 1) * E * sizeof(int32_t); }
+// Counting grows with the pairs, the three launches' scan with pairs times experts.
+// In us, one launch and three, distinct ids: 8 experts, 65536 pairs 10.9 and 11.4,
+// 131072 17.4 and 14.9; 384 experts, 98304 14.0 and 17.0 (all ids the same 17.6 and
+// 17.7), 131072 17.6 and 19.6 (22 and 20); 1024 experts, 131072 18.2 and 26.
+int one_max_pairs(int E) {
+  const int most = 65536 + 128 * E;
+  return most < 131072 ? most : 131072;
+}
 
-// From how many pairs of each expert lie before the range (count[0, E)) and in it
-// or past it (count[E, 2 E)): counts, offsets, and in count[0, E) the range's
-// first row of each expert.  By the whole workgroup.
-__device__ __forceinline__ void bases_from_counts(int32_t* count, int E, int32_t* counts,
-                                                  int32_t* offsets, int32_t* wave_sum) {
+// A copy's counter holds the pairs before the range in its lower 16 bits and the
+// others above: eight lanes of a wave share a copy, so neither passes 131072 / 8.
+// Ints from one copy to the next: odd, so that an expert's lie in different banks.
+__host__ __device__ constexpr int one_copy(int E) { return E | 1; }
+
+// bases and permute_block's tables, before them, in the same place, the copies
+// (k >= 4 experts at least, so 18 E ints are more than 8 (E + 1))
+size_t one_lds(int E) { return size_t(1 + kOneWaves + 1) * E * sizeof(int32_t); }
+
+// From how many pairs of expert threadIdx.x lie before the range and how many in it
+// or past it (0 from E on; E <= 1024): counts, offsets, and in base[0, E) the range's
+// first row of each expert.  By the whole workgroup, whose threads may read what
+// lies at base until they call it.
+__device__ __forceinline__ void bases_from_counts(int before, int rest, int32_t* base, int E,
+                                                  int32_t* counts, int32_t* offsets,
+                                                  int32_t* wave_sum) {
   const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
-  // E <= 1024: one expert a thread
-  const int before = tid < E ? count[tid] : 0;
-  const int total = before + (tid < E ? count[E + tid] : 0);
+  const int total = before + rest;
   const int incl = wave_incl_scan(total);
   if (lane == kWave - 1) wave_sum[wave] = incl;
   __syncthreads();
@@ -140,7 +158,7 @@ __device__ __forceinline__ void bases_from_counts(int32_t* count, int E, int32_t
     all += wave_sum[w];
   }
   if (tid < E) {
-    count[tid] = run + before;
+    base[tid] = run + before;
     if (blockIdx.x == 0) {
       counts[tid] = total;
       offsets[tid] = run;
@@ -162,7 +180,9 @@ __global__ __launch_bounds__(kOneWaves * kWave) void k_perm_one(const int32_t* _
   const int tid = threadIdx.x;
   int r0, r1;
   range_of(R, nr, blockIdx.x, r0, r1);
-  for (int e = tid; e < 2 * E; e += NT) smem[e] = 0;
+  const int copy = one_copy(E);
+  int32_t* mine = smem + ((lane_id() + (lane_id() >> 3)) & (kOneCopies - 1)) * copy;
+  for (int e = tid; e < kOneCopies * copy; e += NT) smem[e] = 0;
   __syncthreads();
   for (int p0 = tid; p0 < R; p0 += NT * kOneBatch) {
     int id[kOneBatch];
@@ -171,13 +191,22 @@ __global__ __launch_bounds__(kOneWaves * kWave) void k_perm_one(const int32_t* _
 #pragma unroll
     for (int i = 0; i < kOneBatch; ++i) {
       const int p = p0 + NT * i;
-      if (p < R && unsigned(id[i]) < unsigned(E)) atomicAdd(&smem[id[i] + (p < r0 ? 0 : E)], 1);
+      if (p < R && unsigned(id[i]) < unsigned(E)) atomicAdd(&mine[id[i]], p < r0 ? 1 : 1 << 16);
     }
   }
   __syncthreads();
-  bases_from_counts(smem, E, counts, offsets, wave_sum);
+  int before = 0, rest = 0;
+  if (tid < E) {
+#pragma unroll
+    for (int c = 0; c < kOneCopies; ++c) {
+      const int n = smem[c * copy + tid];
+      before += n & 0xffff;
+      rest += n >> 16;
+    }
+  }
+  bases_from_counts(before, rest, smem, E, counts, offsets, wave_sum);
   permute_block<kOneWaves>(ids, r0, r1, E, smem, nullptr, nullptr, sorted_pairs, pair_to_row,
-                           smem + 2 * E, wave_sum);
+                           smem + E, wave_sum);
 }
 
 // The same from the counts of every kCountTokens tokens, a byte an expert (E a
@@ -193,7 +222,7 @@ __global__ __launch_bounds__(kOneWaves * kWave) void k_perm_counted(
   extern __shared__ int32_t smem[];
   __shared__ int32_t wave_sum[kOneWaves];
   __shared__ uint32_t part[4][kCountExperts / 4];        // even and odd experts, before and from here on
-  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + 2 * E);
+  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + E);
   const int tid = threadIdx.x, cols = E / 4, here = blockIdx.x;
   const int pair = here * kCountTokens * k + tid;          // of the first kCountTokens k threads
   const bool owns = tid < kCountTokens * k && pair < R;
@@ -226,13 +255,13 @@ __global__ __launch_bounds__(kOneWaves * kWave) void k_perm_counted(
     for (int i = 0; i < 4; ++i) atomicAdd(&part[i][col], s[i]);
   }
   __syncthreads();
-  for (int e = tid; e < E; e += NT) {
-    const int i = e >> 2, shift = (e & 2) * 8;
-    smem[e] = part[e & 1][i] >> shift & 0xffff;
-    smem[E + e] = part[2 + (e & 1)][i] >> shift & 0xffff;
+  int before = 0, rest = 0;
+  if (tid < E) {
+    const int i = tid >> 2, shift = (tid & 2) * 8;
+    before = part[tid & 1][i] >> shift & 0xffff;
+    rest = part[2 + (tid & 1)][i] >> shift & 0xffff;
   }
-  __syncthreads();
-  bases_from_counts(smem, E, counts, offsets, wave_sum);
+  bases_from_counts(before, rest, smem, E, counts, offsets, wave_sum);
   if (valid) {
     const int row = smem[id] + __popc(mask[id] & ((1u << (tid / k)) - 1u));
     sorted_pairs[row] = pair;
@@ -250,16 +279,18 @@ int ranges_for(int64_t R) {
 
 }  // namespace
 
-// an expert's count fits 16 bits
+// an expert's count fits 16 bits, and the bytes fit the workspace of three launches
+constexpr int kCountedTokens = 1 << 14;
+
 bool permute_counted_fits(int T, int E) {
-  return T <= kOneMaxPairs / 8 && E % 4 == 0 && E <= kCountExperts;
+  return T <= kCountedTokens && E % 4 == 0 && E <= kCountExperts;
 }
 
 hipError_t launch_permute_counted(const int32_t* ids, int T, int E, int k, const uint32_t* bytes,
                                   int32_t* counts, int32_t* offsets, int32_t* sorted_pairs,
                                   int32_t* pair_to_row, hipStream_t s) {
   const int rows = (T + kCountTokens - 1) / kCountTokens;
-  k_perm_counted<<<rows, kOneWaves * kWave, size_t(3) * E * sizeof(int32_t), s>>>(ids, T * k, E, k, bytes, rows, counts, offsets,
+  k_perm_counted<<<rows, kOneWaves * kWave, size_t(2) * E * sizeof(int32_t), s>>>(ids, T * k, E, k, bytes, rows, counts, offsets,
                                                             sorted_pairs, pair_to_row);
   return hipGetLastError();
 }
@@ -273,8 +304,8 @@ hipError_t launch_permute(const int32_t* ids, int T, int E, int k, int32_t* coun
                           void* workspace, hipStream_t s) {
   const int R = T * k;
   const int nr = ranges_for(R);
-  if (nr > 0 && k >= 4 && R <= kOneMaxPairs) {
-    static std::atomic<bool> set[kMaxDevices];   // 19 E ints, E up to 1024: above 64 KB
+  if (nr > 0 && k >= 4 && R <= one_max_pairs(E)) {
+    static std::atomic<bool> set[kMaxDevices];   // 18 E ints, E up to 1024: above 64 KB
     const hipError_t e = lds_limit_once(reinterpret_cast<const void*>(&k_perm_one), int(one_lds(1024)), set);
     if (e != hipSuccess) return e;
     const int n = (R + kOneRange - 1) / kOneRange < 256 ? (R + kOneRange - 1) / kOneRange : 256;
