@@ -277,8 +277,15 @@ __device__ __forceinline__ float lane_above(float v) {
 // does not tell.  With h the larger logit of the two and d their distance
 //   sigmoid(h) - sigmoid(h - d) = s(h) u(h - d) (1 - exp(-d)),
 //   softmax the same without u,
-// a product of factors known to 2^-20 (softmax: 2^-17), however close the two
-// scores are.  All lanes call it: a lane reads its neighbour's registers.
+// a product of factors known however close the two scores are.  Its error, relative,
+// in units of 2^-24: of an exponential 2.2 (its instruction 2, its argument 0.2), of
+// 1/(1+q) 4.1 at most and of q/(1+q) 5.2 (the exponential's, a sum's 1, the
+// reciprocal's 2, a product's 1; a score and a u are never both of the second form);
+// of 1 - exp(-d) 7.6 at most: d's rounding 1, the series' last steps 2.3 and its
+// rest d^8 / 8! 4.3, or 4.9 by the exponential; two products 2.  Together 19, and
+// 24 are taken.  Softmax: the sum's 56 (below) in the place of a reciprocal's, 68
+// together, and 128 are taken.  All lanes call it: a lane reads its neighbour's
+// registers.
 __device__ __forceinline__ int order_of(float l, float b, int id, float s, float u, bool biased,
                                         bool sigmoid) {
   const float nl = lane_above(l), nb = lane_above(b), ns = lane_above(s), nu = lane_above(u);
@@ -299,7 +306,7 @@ __device__ __forceinline__ int order_of(float l, float b, int id, float s, float
   const float db = b - nb;
   // values that fp64 does not tell apart are equal: left to it, as are scores that
   // fp32 holds with few digits
-  const float err = (sigmoid ? 0x1p-20f : 0x1p-17f) * ds + 0x1p-22f * fabsf(db) +
+  const float err = (sigmoid ? 0x1.8p-20f : 0x1p-17f) * ds + 0x1p-22f * fabsf(db) +
                     0x1p-51f * (fabsf(s) + fabsf(b)) + 0x1p-140f;
   const float x = (up ? ds : -ds) + db;
   if (l == nl && b == nb) return by_id;
@@ -355,8 +362,9 @@ __device__ __forceinline__ void score_token(const float* __restrict__ row,
       c[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v[i] * -1.4426950408889634f));
   } else if (r.norm && scored) {
     // with d = l - top, of exp(d): 2^-23 (|d| + 1) relative, so at most 2^-23 in
-    // all; of the sum: 2^-23 (1 + the mean of |d| by weight, at most ln E, and a
-    // quarter of its 38 additions); of each s at most 2^-23 (3 + 7 + 10) / total
+    // all; of the sum: 2^-23 (1 + the mean of |d| by weight, at most ln E, and half
+    // of its 38 additions), 56 units of 2^-24 with the reciprocal's; of each s at
+    // most 2^-23 (3 + 7 + 19) / total
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NPER; ++i) {
