@@ -503,7 +503,9 @@ int moe_route_scored(const float* logits, const float* bias, int T, int E, int k
 
 /*
  * moe_route_scored_permute — moe_route_scored followed by moe_permute, in one
- * call (one launch for T <= 16).  Arguments and workspace as those two calls;
+ * call.  It is one launch for T <= 16 where a group has at most eight experts
+ * for each of its lanes (64 / groups, rounded down to a power of two): every
+ * E <= 256, and 384 in any number of groups; two or more else.  Arguments and workspace as those two calls;
  * results are theirs, bit for bit.
  */
 int moe_route_scored_permute(const float* logits, const float* bias, int T, int E, int k,
