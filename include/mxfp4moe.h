@@ -491,8 +491,10 @@ int dflash_verify_probs(const void* target_probs, const void* draft_probs, int d
  * fp64's rounding of another may be taken for equal or for the other side.
  * Renormalised weights hold where every chosen score underflows.  Weights are
  * within 2^-18 of the rule's, relative (below fp32's normal range, before the
- * factor, 2^-148 times it).  Deterministic.  1 <= k <= min(32, topk_groups E/groups),
- * E <= 1024; an unknown score is MXM_ERR_DTYPE, all else MXM_ERR_SHAPE.
+ * factor, 2^-148 times it).  Deterministic for one T and one alignment of logits
+ * and bias; from 4096 tokens on sums may run in another order than below, so that
+ * a token's weights, not its ids, may differ between the two in their last bits.
+ * 1 <= k <= min(32, topk_groups E/groups), E <= 1024; an unknown score is MXM_ERR_DTYPE, all else MXM_ERR_SHAPE.
  * The pages give 384 experts with 8 active per token and no scoring rule; these
  * are the rules of layers that balance experts by a bias or keep tokens to a
  * few groups of them.
@@ -555,7 +557,8 @@ size_t lora_add_workspace_bytes(int M, int K, int N, int S, int r);
  *               initialisation.  Calls that share one must not overlap
  * Products are exact and sums, the scaled a x among them, are fp32; a bf16 y
  * is rounded once (RNE).  y overlaps no input.  What is infinite or NaN in a row
- * of x, a or y stays in the rows that read it; b is taken to be finite.
+ * of x, a or y stays in the rows that read it; b is taken to be finite (where
+ * a row meets an infinite one, y becomes NaN).
  * Deterministic.  K a multiple of 8 up to 2^17, N up to 2^17, M up to 2^20, S up
  * to 1024, r up to 128; x, a and b 16-byte aligned.
  * Not on the pages: serving many fine-tuned variants of one set of weights.

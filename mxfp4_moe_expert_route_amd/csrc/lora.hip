@@ -770,7 +770,8 @@ hipError_t launch_fused(const LoraProblem& p, int rows, int places, hipStream_t 
 // One launch wherever it is not much slower: a workgroup reads (ms + nr) 32 K bytes
 // for its t, at 60 to 80 GB/s, and every range of columns reads them again.  With
 // a workgroup for nearly every CU from the row tiles alone there is one range.  In
-// us, one launch and two, of which the second costs the caller 3 more: 8 rows of K =
+// us, one launch and two, of which the second costs a caller 3 more that does not
+// replay a graph (who does would have two be the faster for few rows): 8 rows of K =
 // 6144, N = 4096, rank 16 9.1 and 7.3; of N = 6144, rank 64 18 and 8.7; 8192 rows of
 // rank 64 50 and 59.
 bool fused(const LoraProblem& p) {

@@ -337,7 +337,8 @@ int per_lane(const ScoreRule& r) { return (r.size + (1 << r.lanes_log2) - 1) >> 
 
 // The kernel of four tokens a wave: whole vectors of logits, four lanes a group at
 // least, of 32 experts at most.  In us, it and a wave a token, 384 experts in 8
-// groups: 2048 tokens 6.5 and 5.6, 4096 6.5 and 7.4, 8192 8.0 and 11.0.
+// groups: 2048 tokens 6.3 and 5.5, 4096 6.5 and 7.1, 8192 7.7 and 10.6; with a token
+// left to score_token, as in two of three inputs of 8192, 11 to 15 and 11 to 12.
 bool takes_rows(int T, const ScoreRule& r, const float* logits, const float* bias) {
   return T >= 4096 && r.k <= kRowPicks && r.lanes_log2 >= 2 && per_lane(r) <= 8 && r.size % 4 == 0 &&
          r.keep * r.size >= r.k + 2 && reinterpret_cast<uintptr_t>(logits) % 16 == 0 &&
